@@ -93,8 +93,9 @@ typedef enum {
   FS_ERR_CUDA = 12,            /* a CUDA runtime call failed (see fs_last_cuda_error) */
   FS_ERR_ALIGNMENT = 13,       /* a device pointer is not 4-byte aligned */
   FS_ERR_OPTION = 14,          /* an fs_solve_options field is out of range */
-  FS_ERR_DEVICE_MEMORY = 15    /* the device could not commit the static scratch array of
+  FS_ERR_DEVICE_MEMORY = 15,   /* the device could not commit the static scratch array of
                                   fs_potentials_noalloc when its module was loaded */
+  FS_ERR_DTYPE = 16            /* an element type is unknown or not one the call takes */
 } fs_status;
 
 /* Human-readable name of a status code (static storage, never NULL). */
@@ -381,6 +382,129 @@ FS_API fs_status fs_marginal_residual(const fs_problem* p, const float* f, const
 #define FS_NOALLOC_SCRATCH_BYTES (20u << 20)
 FS_API fs_status fs_potentials_noalloc(const fs_problem* p, int32_t n_iters, const float* g_init,
                                        float* f, float* g, fs_stream_t stream);
+
+/*
+ * Row-softmax operators on a given score matrix
+ * ---------------------------------------------
+ * The half-iterations above are log-sum-exps over rows of a score matrix that is formed on the
+ * fly. The calls below read one that the caller has (a language model's logits, a router's
+ * logits), or form one from states and an embedding, and return what is read off its row
+ * softmax. They differ from the solves in one way: they are asynchronous. A call checks its
+ * arguments on the host, enqueues its work on `stream` and returns; nothing is read back, so a
+ * call may be captured into a CUDA graph, and a CUDA error of the work itself shows at the
+ * caller's next synchronisation. The current device must be the one that holds the data.
+ * rows == 0 is allowed (nothing is written). A bad value inside the data (NaN, a token number
+ * out of range) never reads or writes out of bounds; it comes back as NaN where each call says
+ * so. Calls may run concurrently on different streams; each needs a workspace of its own while
+ * it runs (where one is taken), and two CUDA graphs that hold the same workspace must not run
+ * at once.
+ */
+typedef enum { FS_F32 = 0, FS_F16 = 1, FS_BF16 = 2 } fs_dtype;
+
+/* A row-major matrix: element (i, j) at data + i * ld + j. */
+typedef struct {
+  const void* data; /* device, aligned to its element */
+  int64_t rows;     /* >= 0, < 2^31 */
+  int64_t cols;     /* >= 1, < 2^31 */
+  int64_t ld;       /* >= cols */
+  int32_t dtype;    /* fs_dtype */
+} fs_matrix;
+
+/*
+ * Log probabilities of given tokens. With u = z / eps and lse_i = log sum_j e^(u_ij):
+ *   logp_i = u_(i, ids_i) - lse_i,   entropy_i = -sum_j p_ij log p_ij,   p_ij = e^(u_ij - lse_i),
+ * and the `top` (0 .. FS_MAX_TOP, <= cols) most probable columns of each row, largest first,
+ * equal scores by the lower index: top_logp and top_ids, (rows, top). One read of z, sums in
+ * float32. ids (rows): int32, or int64 when ids_64 is 1.
+ * A negative id marks a row that nobody asks about: it is not read; logp, entropy and lse are
+ * 0, top_logp -inf, top_ids -1. An id >= cols gives logp NaN (the rest of the row stands). A
+ * score of -inf has probability 0; a row of nothing else gives lse and logp -inf, entropy 0.
+ * NaN or +inf in a row makes its results NaN (top_ids then order what is not NaN, and hold -1
+ * in places left over).
+ * lse and stats may be NULL; stats (rows, 2 floats: the row's largest z, and lse - that / eps)
+ * is what the gradient needs.
+ */
+#define FS_MAX_TOP 32
+FS_API fs_status fs_token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
+                                   int32_t top, float* logp, float* entropy, float* lse,
+                                   float* stats, float* top_logp, int32_t* top_ids,
+                                   fs_stream_t stream);
+
+/*
+ * Gradient of those for z: grad (rows, cols), element type of z, row stride ld_grad, must not
+ * overlap z. g_logp, g_entropy, g_lse (rows) and g_top (rows, top) are the incoming gradients,
+ * NULL for 0; stats, entropy and (with g_top) top_ids come from the forward call.
+ *   eps dz_ij = p_ij (c_i - g_entropy_i (log p_ij + entropy_i)) + g_logp_i [j = ids_i]
+ *               + sum_k g_top_ik [j = top_ids_ik],   c_i = g_lse_i - g_logp_i - sum_k g_top_ik,
+ * summed in float32 and rounded once. Rows with a negative id, and rows of nothing but -inf,
+ * get 0; an id >= cols makes the row NaN.
+ */
+FS_API fs_status fs_token_logprobs_grad(const fs_matrix* z, float eps, const void* ids,
+                                        int32_t ids_64, int32_t top, const int32_t* top_ids,
+                                        const float* stats, const float* entropy,
+                                        const float* g_logp, const float* g_entropy,
+                                        const float* g_lse, const float* g_top, void* grad,
+                                        int64_t ld_grad, fs_stream_t stream);
+
+/*
+ * Routing to experts. z (rows, experts <= FS_MAX_EXPERTS): a token's logits. With scores s =
+ * softmax(z) or sigmoid(z) and c_j = s_j + bias_j (bias (experts) or NULL): of the `groups`
+ * groups of consecutive experts (experts divisible by groups, groups <= 32) the top_groups with
+ * the largest sums of their two largest c are kept, of their experts the k (1 .. FS_MAX_ROUTE_K,
+ * <= top_groups * experts / groups) largest c are picked, largest first, equal ones by the lower
+ * index: ids (rows, k). weights (rows, k): scale s_a / (sum of the picked s), or scale s_a when
+ * renormalize is 0. The bias takes part in the choice only; the g of fs_balance is one. The
+ * choice is that of c in 64 bits; weights are float32.
+ * An expert whose logit or bias is -inf is closed: it is never picked, and places left over
+ * hold id -1 and weight 0. A row with NaN (or +inf under softmax) gets ids -1 and weights NaN.
+ * load (experts, int32) or NULL: how many rows picked each expert.
+ */
+#define FS_MAX_EXPERTS 1024
+#define FS_MAX_ROUTE_K 31
+typedef enum { FS_SCORE_SOFTMAX = 0, FS_SCORE_SIGMOID = 1 } fs_score_kind;
+
+typedef struct {
+  int32_t k;
+  int32_t score;       /* fs_score_kind */
+  int32_t groups;      /* 1: no groups */
+  int32_t top_groups;  /* 1 .. groups */
+  int32_t renormalize; /* 0 or 1 */
+  float scale;         /* finite */
+  const float* bias;   /* device (experts) or NULL */
+} fs_route_options;
+
+FS_API fs_status fs_route(const fs_matrix* z, const fs_route_options* opt, float* weights,
+                          int32_t* ids, int32_t* load, fs_stream_t stream);
+
+/*
+ * Gradient of the weights for z at the given choice: grad (rows, experts), contiguous, element
+ * type of z. ids and weights are the forward call's, g_weights (rows, k) the incoming gradient.
+ */
+FS_API fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt,
+                               const float* weights, const int32_t* ids, const float* g_weights,
+                               void* grad, fs_stream_t stream);
+
+/*
+ * Sinkhorn potentials of a given score matrix: the alternating updates of fs_potentials for
+ * C = -s, s = softmax(z) or sigmoid(z) by row, uniform row weights and column weights
+ * proportional to load (experts, >= 0; NULL for uniform; it is normalised):
+ *   g <- g_init (or 0);  repeat n_iters times:
+ *     f_i <- -eps log sum_j b_j e^((s_ij + g_j)/eps),   b_j = load_j / sum load
+ *     g_j <- -eps log mean_i e^((s_ij + f_i)/eps)
+ * f (rows), g (experts), float32. The plan b_j e^((s_ij + f_i + g_j)/eps) / rows has the load's
+ * column sums, and its largest entry in a row is where s_ij + g_j + eps log b_j is: with that
+ * bias (g alone for a uniform load) fs_route's first pick follows the load as far as the plan
+ * is sharp (small eps); for k > 1 the further picks are evened out only roughly.
+ * Logits of -inf are closed (e^.. = 0), a row of nothing else takes no part and gets f = 0, a
+ * column closed to every row g = 0, a column of load 0 g = -inf. NaN in z, or a load with a
+ * negative entry, NaN or sum 0, makes the outputs NaN. All iterations run in one cooperative
+ * launch; its waits are bounded (2 s), and if one expires f and g are NaN.
+ * ws: fs_balance_workspace_bytes(z) bytes (0 for a shape that is not taken), 256-byte aligned.
+ */
+FS_API size_t fs_balance_workspace_bytes(const fs_matrix* z);
+FS_API fs_status fs_balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
+                            const float* load, const float* g_init, float* f, float* g, void* ws,
+                            size_t ws_bytes, fs_stream_t stream);
 
 /*
  * Checks of the error path (SinkSLOT README, "Tensor Contract": bad states raise rather than

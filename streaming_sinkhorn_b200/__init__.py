@@ -21,7 +21,7 @@ __all__ = ["potentials", "cost", "grad_x", "marginal_residual", "solve_host", "w
            "workspace_invalidate",
            "FsError", "timing_enable", "timing_reset", "timing_get", "launch_count",
            "screening_enable", "solve", "transport_apply", "hvp", "SamplesLoss",
-           "sinkhorn_divergence", "solve_multiscale"]
+           "sinkhorn_divergence", "solve_multiscale", "token_logprobs", "route", "balance"]
 
 
 class FsError(RuntimeError):
@@ -39,7 +39,7 @@ class FsValueError(FsError, ValueError):
     """Invalid inputs: bad shapes, weights, eps, iteration count or workspace."""
 
 
-_INPUT_ERRORS = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 13}
+_INPUT_ERRORS = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 13, 16}
 
 
 def _raise(status: int):
@@ -431,3 +431,4 @@ def timing_get() -> dict:
 
 
 from .loss import SamplesLoss  # noqa: E402  (uses the functions above)
+from .rows import balance, route, token_logprobs  # noqa: E402

@@ -17,7 +17,7 @@ STATUS = {
     5: "FS_ERR_NEGATIVE_WEIGHT", 6: "FS_ERR_NONFINITE_INPUT", 7: "FS_ERR_MASS_MISMATCH",
     8: "FS_ERR_ZERO_MASS", 9: "FS_ERR_UNSUPPORTED_D", 10: "FS_ERR_WORKSPACE",
     11: "FS_ERR_TIMEOUT", 12: "FS_ERR_CUDA", 13: "FS_ERR_ALIGNMENT", 14: "FS_ERR_OPTION",
-    15: "FS_ERR_DEVICE_MEMORY",
+    15: "FS_ERR_DEVICE_MEMORY", 16: "FS_ERR_DTYPE",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -29,8 +29,15 @@ EXPORTS = (
     "fs_potentials_noalloc", "fs_screening_enable", "fs_solve", "fs_transport_workspace_bytes",
     "fs_transport_apply", "fs_hvp", "fs_divergence_workspace_bytes", "fs_divergence",
     "fs_multiscale_workspace_bytes", "fs_solve_multiscale", "fs_workspace_invalidate",
-    "fs_inject_error_word", "fs_check_bounded_wait",
+    "fs_inject_error_word", "fs_check_bounded_wait", "fs_token_logprobs",
+    "fs_token_logprobs_grad", "fs_route", "fs_route_grad", "fs_balance_workspace_bytes",
+    "fs_balance",
 )
+
+# Limits of the row-softmax operators (include/fs.h).
+FS_MAX_TOP = 32
+FS_MAX_EXPERTS = 1024
+FS_MAX_ROUTE_K = 31
 
 VARIANTS = {"alternating": 0, "symmetric": 1}
 STOP_MODES = {"fixed": 0, "marginal": 1, "potential": 2}
@@ -74,6 +81,21 @@ class fs_hvp_options(ctypes.Structure):
 
 class fs_hvp_report(ctypes.Structure):
     _fields_ = [("cg_iters", ctypes.c_int32), ("cg_rel_residual", ctypes.c_double)]
+
+
+class fs_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class fs_route_options(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
 class fs_timing_entry(ctypes.Structure):
@@ -151,6 +173,19 @@ def load():
     lib.fs_inject_error_word.restype = None
     lib.fs_check_bounded_wait.argtypes = [ctypes.c_int64, vp, sz, vp]
     lib.fs_check_bounded_wait.restype = ctypes.c_int
+    M, f32 = ctypes.POINTER(fs_matrix), ctypes.c_float
+    R = ctypes.POINTER(fs_route_options)
+    lib.fs_token_logprobs.argtypes = [M, f32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.fs_token_logprobs_grad.argtypes = [M, f32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                           ctypes.c_int64, vp]
+    lib.fs_route.argtypes = [M, R, vp, vp, vp, vp]
+    lib.fs_route_grad.argtypes = [M, R, vp, vp, vp, vp, vp]
+    lib.fs_balance_workspace_bytes.argtypes = [M]
+    lib.fs_balance_workspace_bytes.restype = sz
+    lib.fs_balance.argtypes = [M, i32, f32, i32, vp, vp, vp, vp, vp, sz, vp]
+    for fn in (lib.fs_token_logprobs, lib.fs_token_logprobs_grad, lib.fs_route,
+               lib.fs_route_grad, lib.fs_balance):
+        fn.restype = ctypes.c_int
     lib.fs_launch_count.argtypes = []
     lib.fs_launch_count.restype = ctypes.c_int64
     _lib = lib

@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfs.so")
-SOURCES = ["fs_api.cu", "fs_noalloc.cu"]
+OBJ = os.path.join(HERE, "_build")
+SOURCES = ["fs_api.cu", "fs_noalloc.cu", "fs_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -38,17 +39,44 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def _object_up_to_date(obj: str, dep: str) -> bool:
+    """Whether obj is newer than every file that its last compilation read (nvcc's -MD list)."""
+    if not (os.path.exists(obj) and os.path.exists(dep)):
+        return False
+    t = os.path.getmtime(obj)
+    names = open(dep).read().split(":", 1)[1].replace("\\\n", " ").split()
+    return all(os.path.exists(f) and os.path.getmtime(f) <= t for f in names)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the sources side by side (only those that changed, unless force) and links."""
     if not force and up_to_date():
         return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),
-           "--expt-relaxed-constexpr", "-o", tmp]
+    os.makedirs(OBJ, exist_ok=True)
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+             "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),
+             "--expt-relaxed-constexpr"]
     if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
-    subprocess.run(cmd, check=True)
+        flags += ["-Xptxas", "-v"]
+    jobs, objects = [], []
+    for src in SOURCES:
+        obj = os.path.join(OBJ, src + ".o")
+        objects.append(obj)
+        if not force and _object_up_to_date(obj, obj + ".d"):
+            continue
+        tmp = obj + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *flags, "-MD", "-MF", obj + ".d", "-c", os.path.join(CSRC, src), "-o", tmp]
+        jobs.append((subprocess.Popen(cmd), cmd, tmp, obj))
+    failed = None
+    for proc, cmd, tmp, obj in jobs:
+        if proc.wait() != 0:
+            failed = failed or subprocess.CalledProcessError(proc.returncode, cmd)
+        else:
+            os.replace(tmp, obj)
+    if failed:
+        raise failed
+    tmp = LIB + f".tmp{os.getpid()}"
+    subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objects], check=True)
     os.replace(tmp, LIB)
     return LIB
 

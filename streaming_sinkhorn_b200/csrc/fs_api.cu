@@ -2290,6 +2290,9 @@ void record_cuda_error(const char* what, cudaError_t e) {
   snprintf(g_cuda_err, sizeof(g_cuda_err), "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Adds another translation unit's kernel launches to fs_launch_count.
+void count_launches(int64_t k) { g_launches.fetch_add(k, std::memory_order_relaxed); }
+
 }  // namespace fs
 
 extern "C" {
@@ -2313,6 +2316,7 @@ const char* fs_status_string(fs_status s) {
     case FS_ERR_ALIGNMENT: return "FS_ERR_ALIGNMENT: device pointers must be 4-byte aligned";
     case FS_ERR_DEVICE_MEMORY:
       return "FS_ERR_DEVICE_MEMORY: the device could not commit the library's static scratch array";
+    case FS_ERR_DTYPE: return "FS_ERR_DTYPE: unknown or unsupported element type";
   }
   return "unknown fs_status";
 }

@@ -1,0 +1,403 @@
+// fs_rows.cu -- C ABI of the row-softmax operators on a given score matrix (include/fs.h):
+// argument checks, launch plans and launches. Nothing here waits for the device.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fs_balance.cuh"
+#include "fs_host.h"
+#include "fs_route.cuh"
+#include "fs_tokens.cuh"
+
+namespace fs {
+namespace {
+
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+
+fs_status check_matrix(const fs_matrix* z) {
+  if (!z) return FS_ERR_NULL;
+  if (z->dtype < FS_F32 || z->dtype > FS_BF16) return FS_ERR_DTYPE;
+  if (z->rows < 0 || z->rows > kMaxInt || z->cols < 1 || z->cols > kMaxInt || z->ld < z->cols ||
+      z->ld > (INT64_MAX >> 3) / std::max<int64_t>(z->rows, 1))
+    return FS_ERR_SHAPE;
+  if (z->rows > 0 && !z->data) return FS_ERR_NULL;
+  if (!aligned(z->data, z->dtype == FS_F32 ? 4 : 2)) return FS_ERR_ALIGNMENT;
+  return FS_OK;
+}
+
+fs_status check_eps(float eps) {
+  // 1 / eps is used as a factor
+  return std::isfinite(eps) && eps > 0.0f && std::isfinite(1.0f / eps) ? FS_OK : FS_ERR_EPS;
+}
+
+// Calls f with a null pointer of the matrix's element type.
+template <typename F>
+fs_status by_type(int32_t dtype, F&& f) {
+  switch (dtype) {
+    case FS_F32: return f(static_cast<float*>(nullptr));
+    case FS_F16: return f(static_cast<__half*>(nullptr));
+    default: return f(static_cast<__nv_bfloat16*>(nullptr));
+  }
+}
+
+// CTAs per row of the forward pass. One read of the matrix wants about two CTAs on every SM;
+// with fewer rows than that a row is shared by a cluster, while each CTA keeps at least one
+// full round of vectors.
+int token_cluster(int64_t rows, int64_t cols, int vec) {
+  const int64_t sms = current_sms();
+  int c = 1;
+  while (c < kTokenMaxCluster && rows * c < 2 * sms &&
+         cols >= 2ll * c * kTokenThreads * vec)
+    c *= 2;
+  return c;
+}
+
+fs_status token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
+                         int32_t top, float* logp, float* entropy, float* lse, float* stats,
+                         float* top_logp, int32_t* top_ids, cudaStream_t st) {
+  fs_status s = check_matrix(z);
+  if (s != FS_OK) return s;
+  if ((s = check_eps(eps)) != FS_OK) return s;
+  if (top < 0 || top > FS_MAX_TOP || top > z->cols || (ids_64 != 0 && ids_64 != 1))
+    return FS_ERR_OPTION;
+  if (z->rows == 0) return FS_OK;
+  if (!ids || !logp || !entropy || (top > 0 && (!top_logp || !top_ids))) return FS_ERR_NULL;
+  if (!aligned(ids, ids_64 ? 8 : 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(stats, 8) || !aligned(top_logp, 4) || !aligned(top_ids, 4))
+    return FS_ERR_ALIGNMENT;
+  TokenParams P{};
+  P.z = z->data;
+  P.ld = z->ld;
+  P.ids = ids;
+  P.rows = z->rows;
+  P.cols = static_cast<int32_t>(z->cols);
+  P.ids_wide = ids_64;
+  P.top = top;
+  P.inv_eps = 1.0f / eps;
+  P.logp = logp;
+  P.entropy = entropy;
+  P.lse = lse;
+  P.stats = reinterpret_cast<float2*>(stats);
+  P.top_logp = top_logp;
+  P.top_ids = top_ids;
+  return by_type(z->dtype, [&](auto* t) -> fs_status {
+    using T = std::remove_pointer_t<decltype(t)>;
+    const int c = token_cluster(z->rows, z->cols, Elem<T>::kVec);
+    const dim3 grid(static_cast<unsigned>(z->rows * c));
+    auto fn = top > 0 ? token_logprobs_kernel<T, true> : token_logprobs_kernel<T, false>;
+    return launch("fs_token_logprobs", fn, grid, kTokenThreads, 0, st, c, P, c);
+  });
+}
+
+fs_status token_logprobs_grad(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
+                              int32_t top, const int32_t* top_ids, const float* stats,
+                              const float* entropy, const float* g_logp, const float* g_entropy,
+                              const float* g_lse, const float* g_top, void* grad, int64_t ld_grad,
+                              cudaStream_t st) {
+  fs_status s = check_matrix(z);
+  if (s != FS_OK) return s;
+  if ((s = check_eps(eps)) != FS_OK) return s;
+  if (top < 0 || top > FS_MAX_TOP || top > z->cols || (ids_64 != 0 && ids_64 != 1))
+    return FS_ERR_OPTION;
+  if (ld_grad < z->cols || ld_grad > (INT64_MAX >> 3) / std::max<int64_t>(z->rows, 1))
+    return FS_ERR_SHAPE;
+  if (z->rows == 0) return FS_OK;
+  if (!ids || !stats || !entropy || !grad || (top > 0 && g_top && !top_ids)) return FS_ERR_NULL;
+  if (!aligned(ids, ids_64 ? 8 : 4) || !aligned(stats, 8) || !aligned(entropy, 4) ||
+      !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(g_lse, 4) || !aligned(g_top, 4) ||
+      !aligned(top_ids, 4) || !aligned(grad, z->dtype == FS_F32 ? 4 : 2))
+    return FS_ERR_ALIGNMENT;
+  TokenGradParams P{};
+  P.z = z->data;
+  P.ld = z->ld;
+  P.ids = ids;
+  P.rows = z->rows;
+  P.cols = static_cast<int32_t>(z->cols);
+  P.ids_wide = ids_64;
+  P.top = top;
+  P.inv_eps = 1.0f / eps;
+  P.stats = reinterpret_cast<const float2*>(stats);
+  P.entropy = entropy;
+  P.top_ids = top_ids;
+  P.g_logp = g_logp;
+  P.g_entropy = g_entropy;
+  P.g_lse = g_lse;
+  P.g_top = top > 0 ? g_top : nullptr;
+  P.grad = grad;
+  P.ld_grad = ld_grad;
+  return by_type(z->dtype, [&](auto* t) -> fs_status {
+    using T = std::remove_pointer_t<decltype(t)>;
+    const int64_t per = static_cast<int64_t>(kTokenThreads) * kTokenUnroll * Elem<T>::kVec;
+    const int64_t chunks = (z->cols + per - 1) / per;
+    if (chunks * z->rows > kMaxInt) return FS_ERR_SHAPE;
+    P.chunks = static_cast<int32_t>(chunks);
+    return launch("fs_token_logprobs_grad", token_logprobs_grad_kernel<T>,
+                  dim3(static_cast<unsigned>(chunks * z->rows)), kTokenThreads, 0, st, 1, P);
+  });
+}
+
+// ---- routing --------------------------------------------------------------------------------
+
+fs_status check_route(const fs_matrix* z, const fs_route_options* o) {
+  const fs_status s = check_matrix(z);
+  if (s != FS_OK) return s;
+  if (!o) return FS_ERR_NULL;
+  if (z->cols > FS_MAX_EXPERTS) return FS_ERR_SHAPE;
+  if ((o->score != FS_SCORE_SOFTMAX && o->score != FS_SCORE_SIGMOID) || o->groups < 1 ||
+      o->groups > kRouteMaxGroups || z->cols % o->groups != 0 || o->top_groups < 1 ||
+      o->top_groups > o->groups || o->k < 1 || o->k > FS_MAX_ROUTE_K ||
+      o->k > o->top_groups * (z->cols / o->groups) ||
+      (o->renormalize != 0 && o->renormalize != 1) || !std::isfinite(o->scale))
+    return FS_ERR_OPTION;
+  if (!aligned(o->bias, 4)) return FS_ERR_ALIGNMENT;
+  return FS_OK;
+}
+
+// Experts per lane, rounded up to a power of two: 1 .. 32.
+template <typename F>
+fs_status by_width(int64_t experts, F&& f) {
+  if (experts <= 32) return f(std::integral_constant<int, 1>());
+  if (experts <= 64) return f(std::integral_constant<int, 2>());
+  if (experts <= 128) return f(std::integral_constant<int, 4>());
+  if (experts <= 256) return f(std::integral_constant<int, 8>());
+  if (experts <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+fs_status route(const fs_matrix* z, const fs_route_options* o, float* weights, int32_t* ids,
+                int32_t* load, cudaStream_t st) {
+  fs_status s = check_route(z, o);
+  if (s != FS_OK) return s;
+  if (!aligned(weights, 4) || !aligned(ids, 4) || !aligned(load, 4)) return FS_ERR_ALIGNMENT;
+  if (z->rows > 0 && (!weights || !ids)) return FS_ERR_NULL;
+  if (load) {
+    s = cuda_status(cudaMemsetAsync(load, 0, z->cols * sizeof(int32_t), st), "cudaMemsetAsync");
+    if (s != FS_OK) return s;
+  }
+  if (z->rows == 0) return FS_OK;
+  RouteParams P{};
+  P.z = z->data;
+  P.ld = z->ld;
+  P.rows = z->rows;
+  P.experts = static_cast<int32_t>(z->cols);
+  P.k = o->k;
+  P.groups = o->top_groups == o->groups ? 1 : o->groups;  // all groups kept: no groups
+  P.per_group = P.experts / P.groups;
+  P.top_groups = o->top_groups;
+  P.score = o->score;
+  P.renorm = o->renormalize;
+  P.scale = o->scale;
+  P.bias = o->bias;
+  P.weights = weights;
+  P.ids = ids;
+  P.load = load;
+  // one warp per row; with a load to count, CTAs stay and take several rows each, so that few
+  // histograms are added up
+  int64_t ctas = (z->rows + kRouteWarps - 1) / kRouteWarps;
+  if (load) ctas = std::min<int64_t>(ctas, 8ll * current_sms());
+  const size_t smem = static_cast<size_t>(P.experts) * (kRouteWarps * sizeof(double) + sizeof(int));
+  return by_type(z->dtype, [&](auto* t) -> fs_status {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return by_width(z->cols, [&](auto nl) -> fs_status {
+      constexpr auto fn = route_kernel<T, decltype(nl)::value>;
+      static PerDeviceOnce once;
+      const fs_status a = once.run("cudaFuncSetAttribute", [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    FS_MAX_EXPERTS * (kRouteWarps * 8 + 4));
+      });
+      if (a != FS_OK) return a;
+      return launch("fs_route", fn, dim3(static_cast<unsigned>(ctas)), kRouteWarps * 32, smem, st,
+                    1, P);
+    });
+  });
+}
+
+fs_status route_grad(const fs_matrix* z, const fs_route_options* o, const float* weights,
+                     const int32_t* ids, const float* g_weights, void* grad, cudaStream_t st) {
+  const fs_status s = check_route(z, o);
+  if (s != FS_OK) return s;
+  if (z->rows == 0) return FS_OK;
+  if (!weights || !ids || !g_weights || !grad) return FS_ERR_NULL;
+  if (!aligned(weights, 4) || !aligned(ids, 4) || !aligned(g_weights, 4) ||
+      !aligned(grad, z->dtype == FS_F32 ? 4 : 2))
+    return FS_ERR_ALIGNMENT;
+  RouteGradParams P{};
+  P.z = z->data;
+  P.ld = z->ld;
+  P.rows = z->rows;
+  P.experts = static_cast<int32_t>(z->cols);
+  P.k = o->k;
+  P.score = o->score;
+  P.renorm = o->renormalize;
+  P.scale = o->scale;
+  P.weights = weights;
+  P.ids = ids;
+  P.g_weights = g_weights;
+  P.grad = grad;
+  const int64_t ctas = (z->rows + kRouteWarps - 1) / kRouteWarps;
+  return by_type(z->dtype, [&](auto* t) -> fs_status {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return by_width(z->cols, [&](auto nl) -> fs_status {
+      return launch("fs_route_grad", route_grad_kernel<T, decltype(nl)::value>,
+                    dim3(static_cast<unsigned>(ctas)), kRouteWarps * 32, 0, st, 1, P);
+    });
+  });
+}
+
+// ---- balancing ------------------------------------------------------------------------------
+
+// The launch of one problem: lanes per row, CTAs, and what fits in shared memory.
+struct BalancePlan {
+  int nl, lpt, cols;
+  int ctas, per_cta, resident;
+  size_t smem;
+  size_t off_redo, off_spill, total;  // workspace: sync word, partial sums, redo, spill
+};
+
+constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 80 bytes
+
+BalancePlan balance_plan(int64_t rows, int64_t experts) {
+  BalancePlan p{};
+  p.nl = experts <= 256 ? 8 : experts <= 512 ? 16 : 32;
+  p.lpt = 1;
+  while (p.nl * p.lpt < experts) p.lpt *= 2;
+  p.cols = p.nl * p.lpt;
+  // rows a CTA takes at once; a grid barrier costs as much as a few such steps
+  const int64_t step = (32 / p.lpt) * kBalWarps;
+  const int64_t want = (rows + 2 * step - 1) / (2 * step);
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(want, current_sms()));
+  const int64_t per = std::max<int64_t>(1, (rows + ctas - 1) / ctas);
+  p.per_cta = static_cast<int>(per);
+  p.ctas = static_cast<int>(std::max<int64_t>(1, (rows + per - 1) / per));
+  const size_t fixed = static_cast<size_t>(2 + kBalWarps) * p.cols * 4;
+  const size_t row = static_cast<size_t>(p.cols) * 4;
+  p.resident = static_cast<int>(std::min<int64_t>(per, (kBalSmemBudget - fixed) / row));
+  p.smem = fixed + p.resident * row;
+  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  p.off_redo = 256 + up(2 * static_cast<size_t>(p.ctas) * (p.cols + 1) * 4);
+  p.off_spill = p.off_redo + up(static_cast<size_t>(p.ctas) * p.cols * 8);
+  p.total = p.off_spill + up(static_cast<size_t>(p.ctas) * (p.per_cta - p.resident) * row);
+  return p;
+}
+
+fs_status check_balance(const fs_matrix* z) {
+  const fs_status s = check_matrix(z);
+  if (s != FS_OK) return s;
+  return z->cols > FS_MAX_EXPERTS ? FS_ERR_SHAPE : FS_OK;
+}
+
+template <typename F>
+fs_status by_shape(const BalancePlan& p, F&& f) {
+  using std::integral_constant;
+  if (p.nl == 16) return f(integral_constant<int, 16>(), integral_constant<int, 32>());
+  if (p.nl == 32) return f(integral_constant<int, 32>(), integral_constant<int, 32>());
+  switch (p.lpt) {
+    case 1: return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    case 2: return f(integral_constant<int, 8>(), integral_constant<int, 2>());
+    case 4: return f(integral_constant<int, 8>(), integral_constant<int, 4>());
+    case 8: return f(integral_constant<int, 8>(), integral_constant<int, 8>());
+    case 16: return f(integral_constant<int, 8>(), integral_constant<int, 16>());
+    default: return f(integral_constant<int, 8>(), integral_constant<int, 32>());
+  }
+}
+
+fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters, const float* load,
+                  const float* g_init, float* f, float* g, void* ws, size_t ws_bytes,
+                  cudaStream_t st) {
+  fs_status s = check_balance(z);
+  if (s != FS_OK) return s;
+  if ((s = check_eps(eps)) != FS_OK) return s;
+  if (score != FS_SCORE_SOFTMAX && score != FS_SCORE_SIGMOID) return FS_ERR_OPTION;
+  if (n_iters < 1) return FS_ERR_ITERS;
+  if (z->rows == 0) return FS_OK;
+  if (!f || !g) return FS_ERR_NULL;
+  if (!aligned(load, 4) || !aligned(g_init, 4) || !aligned(f, 4) || !aligned(g, 4))
+    return FS_ERR_ALIGNMENT;
+  const BalancePlan p = balance_plan(z->rows, z->cols);
+  if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  BalanceParams P{};
+  P.z = z->data;
+  P.ld = z->ld;
+  P.rows = z->rows;
+  P.experts = static_cast<int32_t>(z->cols);
+  P.cols = p.cols;
+  P.score = score;
+  P.n_iters = n_iters;
+  P.per_cta = p.per_cta;
+  P.resident = p.resident;
+  P.eps = eps;
+  P.load = load;
+  P.g_init = g_init;
+  P.f = f;
+  P.g = g;
+  P.sync = reinterpret_cast<unsigned*>(base);
+  P.part = reinterpret_cast<float*>(base + 256);
+  P.redo = reinterpret_cast<float2*>(base + p.off_redo);
+  P.spill = reinterpret_cast<float*>(base + p.off_spill);
+  s = cuda_status(cudaMemsetAsync(base, 0, 256, st), "cudaMemsetAsync");
+  if (s != FS_OK) return s;
+  return by_type(z->dtype, [&](auto* t) -> fs_status {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return by_shape(p, [&](auto nl, auto lpt) -> fs_status {
+      constexpr auto fn = balance_kernel<T, decltype(nl)::value, decltype(lpt)::value>;
+      static PerDeviceOnce once;
+      const fs_status a = once.run("cudaFuncSetAttribute", [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kBalSmemBudget));
+      });
+      if (a != FS_OK) return a;
+      return launch("fs_balance", fn, dim3(static_cast<unsigned>(p.ctas)), kBalThreads, p.smem, st,
+                    kCooperative, P);
+    });
+  });
+}
+
+}  // namespace
+}  // namespace fs
+
+extern "C" {
+
+fs_status fs_token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
+                            int32_t top, float* logp, float* entropy, float* lse, float* stats,
+                            float* top_logp, int32_t* top_ids, fs_stream_t stream) {
+  return fs::token_logprobs(z, eps, ids, ids_64, top, logp, entropy, lse, stats, top_logp, top_ids,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+fs_status fs_token_logprobs_grad(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
+                                 int32_t top, const int32_t* top_ids, const float* stats,
+                                 const float* entropy, const float* g_logp, const float* g_entropy,
+                                 const float* g_lse, const float* g_top, void* grad,
+                                 int64_t ld_grad, fs_stream_t stream) {
+  return fs::token_logprobs_grad(z, eps, ids, ids_64, top, top_ids, stats, entropy, g_logp,
+                                 g_entropy, g_lse, g_top, grad, ld_grad,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+fs_status fs_route(const fs_matrix* z, const fs_route_options* opt, float* weights, int32_t* ids,
+                   int32_t* load, fs_stream_t stream) {
+  return fs::route(z, opt, weights, ids, load, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt, const float* weights,
+                        const int32_t* ids, const float* g_weights, void* grad,
+                        fs_stream_t stream) {
+  return fs::route_grad(z, opt, weights, ids, g_weights, grad,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t fs_balance_workspace_bytes(const fs_matrix* z) {
+  if (!z || z->rows < 0 || z->rows > fs::kMaxInt || z->cols < 1 || z->cols > FS_MAX_EXPERTS)
+    return 0;
+  return fs::balance_plan(z->rows, z->cols).total;
+}
+
+fs_status fs_balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
+                     const float* load, const float* g_init, float* f, float* g, void* ws,
+                     size_t ws_bytes, fs_stream_t stream) {
+  return fs::balance(z, score, eps, n_iters, load, g_init, f, g, ws, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,327 @@
+"""Row-softmax operators on a given score matrix: log probabilities of given tokens, routing to
+experts, and the Sinkhorn bias that balances the experts' load.
+
+Only argument marshalling happens here: every number comes from the C ABI. Unlike the solves,
+these calls are asynchronous (they enqueue on the current stream of the data's device and
+return) and can be captured into a CUDA graph. Gradients are analytic and differentiable once.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Any, NamedTuple
+
+from . import _lib, _raise, _torch
+
+
+class TokenLogprobs(NamedTuple):
+    """Result of token_logprobs: float32 tensors (T,), the alternatives (T, top) or None."""
+
+    logprobs: Any
+    entropy: Any
+    lse: Any
+    top_logprobs: Any
+    top_ids: Any
+
+
+class Routing(NamedTuple):
+    """Result of route: weights (T, k) float32, ids (T, k) int32, load (E,) int32 or None."""
+
+    weights: Any
+    ids: Any
+    load: Any
+
+
+class _on:
+    """The data's device as the current one during a library call, and its current stream."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        self.before = cuda.current_device()
+        if self.before != self.index:
+            cuda.set_device(self.index)
+        return _torch()._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            _torch().cuda.set_device(self.before)
+
+
+_dtype_codes = {}
+
+
+def _dtype_code(dtype, name):
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({getattr(torch, n): c for n, c in _lib.DTYPES.items()})
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        kind = ValueError if dtype == _torch().float64 else TypeError
+        raise kind(f"{name} is {dtype}: float32, float16 and bfloat16 are supported")
+    return code
+
+
+def _rows_of(t, name):
+    """``t`` as a row-major matrix the library can read: unit column stride, rows that do not
+    overlap (a copy where it is laid out otherwise)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a 2-D tensor with at least one column")
+    _dtype_code(t.dtype, name)
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        # (a single column or row may carry any stride: it is laid out anew too)
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _matrix(t):
+    return _lib.fs_matrix(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]),
+                          _dtype_codes[t.dtype])
+
+
+def _vector(t, name, n, device, dtypes):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _grad_ptr(g, keep):
+    """Address of an incoming gradient laid out contiguously; ``keep`` holds it alive."""
+    if g is None:
+        return None
+    g = g if g.is_contiguous() else g.contiguous()
+    keep.append(g)
+    return g.data_ptr()
+
+
+# ---- log probabilities of given tokens ---------------------------------------------------------
+
+def _token_forward(logits, ids, eps, top, stats):
+    torch = _torch()
+    n, dev = logits.shape[0], logits.device
+    f32 = torch.float32
+    logp = torch.empty(n, dtype=f32, device=dev)
+    entropy = torch.empty(n, dtype=f32, device=dev)
+    lse = torch.empty(n, dtype=f32, device=dev)
+    st = torch.empty((n, 2), dtype=f32, device=dev) if stats else None
+    tl = torch.empty((n, top), dtype=f32, device=dev) if top else None
+    ti = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
+    with _on(dev) as stream:
+        _raise(_lib.load().fs_token_logprobs(
+            ctypes.byref(_matrix(logits)), eps, ids.data_ptr(), int(ids.dtype == torch.int64), top,
+            logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(st), _ptr(tl), _ptr(ti),
+            stream))
+    return logp, entropy, lse, tl, ti, st
+
+
+class _Functions:
+    """The autograd functions, built on first use (importing the package does not import
+    torch)."""
+
+    token = None
+    routing = None
+
+    @classmethod
+    def get_token(cls):
+        if cls.token is None:
+            torch = _torch()
+            from torch.autograd.function import once_differentiable
+
+            class TokenLogprobsFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, logits, ids, eps, top):
+                    logp, entropy, lse, tl, ti, st = _token_forward(logits, ids, eps, top, True)
+                    ctx.save_for_backward(logits, ids, entropy, st, ti)
+                    ctx.eps, ctx.top = eps, top
+                    ctx.set_materialize_grads(False)
+                    if ti is not None:
+                        ctx.mark_non_differentiable(ti)
+                    return logp, entropy, lse, tl, ti
+
+                @staticmethod
+                @once_differentiable
+                def backward(ctx, g_logp, g_entropy, g_lse, g_top, _):
+                    logits, ids, entropy, st, ti = ctx.saved_tensors
+                    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+                    keep = []
+                    with _on(logits.device) as stream:
+                        _raise(_lib.load().fs_token_logprobs_grad(
+                            ctypes.byref(_matrix(logits)), ctx.eps, ids.data_ptr(),
+                            int(ids.dtype == torch.int64), ctx.top, _ptr(ti), st.data_ptr(),
+                            entropy.data_ptr(), _grad_ptr(g_logp, keep), _grad_ptr(g_entropy, keep),
+                            _grad_ptr(g_lse, keep), _grad_ptr(g_top, keep), grad.data_ptr(),
+                            grad.shape[1], stream))
+                    return grad, None, None, None
+
+            cls.token = TokenLogprobsFunction
+        return cls.token
+
+    @classmethod
+    def get_routing(cls):
+        if cls.routing is None:
+            torch = _torch()
+            from torch.autograd.function import once_differentiable
+
+            class RouteFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, logits, bias, options, load):
+                    weights, ids, counts = _route_forward(logits, bias, options, load)
+                    ctx.save_for_backward(logits, weights, ids)
+                    ctx.options = options
+                    ctx.set_materialize_grads(False)
+                    ctx.mark_non_differentiable(ids)
+                    if counts is not None:
+                        ctx.mark_non_differentiable(counts)
+                    return weights, ids, counts
+
+                @staticmethod
+                @once_differentiable
+                def backward(ctx, g_weights, _ids, _load):
+                    if g_weights is None:
+                        return None, None, None, None
+                    logits, weights, ids = ctx.saved_tensors
+                    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+                    keep = []
+                    with _on(logits.device) as stream:
+                        _raise(_lib.load().fs_route_grad(
+                            ctypes.byref(_matrix(logits)),
+                            ctypes.byref(_lib.fs_route_options(*ctx.options, None)),
+                            weights.data_ptr(), ids.data_ptr(), _grad_ptr(g_weights, keep),
+                            grad.data_ptr(), stream))
+                    return grad, None, None, None
+
+            cls.routing = RouteFunction
+        return cls.routing
+
+
+def _needs_grad(*tensors):
+    return _torch().is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+def token_logprobs(logits, ids, *, eps: float = 1.0, top: int = 0) -> TokenLogprobs:
+    """Log probabilities of given tokens under softmax(logits / eps), with each row's entropy,
+    log-sum-exp and ``top`` most probable columns (fs_token_logprobs): one read of the logits.
+
+    logits: (T, V) float32, float16 or bfloat16, rows any stride apart; ids: (T,) int32 or
+    int64, a negative one marking a row nobody asks about (results 0, top_ids -1, gradient 0);
+    eps: the temperature; top: 0..32 alternatives, largest first, equal ones by the lower
+    index. Differentiable for logits through logprobs, entropy, lse and top_logprobs.
+    """
+    logits = _rows_of(logits, "logits")
+    torch = _torch()
+    ids = _vector(ids, "ids", logits.shape[0], logits.device, (torch.int64, torch.int32))
+    eps, top = float(eps), int(top)
+    if not 0 <= top <= min(_lib.FS_MAX_TOP, logits.shape[1]):
+        raise ValueError(f"top must be 0..{min(_lib.FS_MAX_TOP, logits.shape[1])}, got {top}")
+    if _needs_grad(logits):
+        return TokenLogprobs(*_Functions.get_token().apply(logits, ids, eps, top))
+    return TokenLogprobs(*_token_forward(logits, ids, eps, top, False)[:5])
+
+
+# ---- routing to experts ------------------------------------------------------------------------
+
+def _route_forward(logits, bias, options, load):
+    torch = _torch()
+    n, e = logits.shape
+    dev = logits.device
+    k = options[0]
+    weights = torch.empty((n, k), dtype=torch.float32, device=dev)
+    ids = torch.empty((n, k), dtype=torch.int32, device=dev)
+    counts = torch.empty(e, dtype=torch.int32, device=dev) if load else None
+    with _on(dev) as stream:
+        _raise(_lib.load().fs_route(ctypes.byref(_matrix(logits)),
+                                    ctypes.byref(_lib.fs_route_options(*options, _ptr(bias))),
+                                    weights.data_ptr(), ids.data_ptr(), _ptr(counts), stream))
+    return weights, ids, counts
+
+
+def _score_code(score):
+    if score not in _lib.SCORES:
+        raise ValueError(f"unknown score {score!r}: {sorted(_lib.SCORES)}")
+    return _lib.SCORES[score]
+
+
+def route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
+          top_groups: int = 1, renormalize: bool = True, scale: float = 1.0,
+          load: bool = False) -> Routing:
+    """Routing of tokens to their ``k`` best experts (fs_route).
+
+    logits: (T, E) float32, float16 or bfloat16, E <= 1024. The choice goes by score + bias
+    (bias (E,) float32, the ``g`` of ``balance`` for one) within the ``top_groups`` best of
+    ``groups`` groups, ties by the lower index, decided as in 64 bits; the weights are the
+    scores alone, divided by their sum when ``renormalize``, times ``scale``. With ``load`` the
+    result also counts the rows of each expert. Differentiable for logits through weights.
+    """
+    logits = _rows_of(logits, "logits")
+    e = logits.shape[1]
+    if e > _lib.FS_MAX_EXPERTS:
+        raise ValueError(f"{e} experts: at most {_lib.FS_MAX_EXPERTS} are supported")
+    if bias is not None:
+        bias = _vector(bias.detach(), "bias", e, logits.device, (_torch().float32,))
+    k, groups, top_groups = int(k), int(groups), int(top_groups)
+    if groups < 1 or groups > 32 or e % groups or not 1 <= top_groups <= groups:
+        raise ValueError(f"{top_groups} of {groups} groups of {e} experts: groups must be 1..32 "
+                         "and divide the experts, top_groups 1..groups")
+    most = min(_lib.FS_MAX_ROUTE_K, top_groups * (e // groups))
+    if not 1 <= k <= most:
+        raise ValueError(f"k must be 1..{most}, got {k}")
+    options = (k, _score_code(score), groups, top_groups, int(bool(renormalize)), float(scale))
+    if _needs_grad(logits):
+        return Routing(*_Functions.get_routing().apply(logits, bias, options, bool(load)))
+    return Routing(*_route_forward(logits, bias, options, load))
+
+
+# ---- balancing ---------------------------------------------------------------------------------
+
+def balance(logits, *, score: str = "softmax", eps: float, n_iters: int, load=None, g_init=None):
+    """Sinkhorn potentials (f, g) of the experts' scores (fs_balance): ``n_iters`` alternating
+    updates from g = g_init (or 0), every row of equal mass, the columns' masses proportional
+    to ``load`` (E,) (uniform when omitted). With ``bias=g`` (for a given load b,
+    ``g + eps * log(b)``) the first pick of ``route`` follows that load, the more closely the
+    smaller eps (in units of the scores).
+
+    logits: (T, E) float32, float16 or bfloat16, E <= 1024. Returns f (T,) and g (E,), float32,
+    not differentiable.
+    """
+    torch = _torch()
+    logits = _rows_of(logits.detach() if isinstance(logits, torch.Tensor) else logits, "logits")
+    n, e = logits.shape
+    dev = logits.device
+    if e > _lib.FS_MAX_EXPERTS:
+        raise ValueError(f"{e} experts: at most {_lib.FS_MAX_EXPERTS} are supported")
+    if n < 1:
+        raise ValueError("logits must have at least one row")
+    if load is not None:
+        load = _vector(load.detach(), "load", e, dev, (torch.float32,))
+    if g_init is not None:
+        g_init = _vector(g_init.detach(), "g_init", e, dev, (torch.float32,))
+    f = torch.empty(n, dtype=torch.float32, device=dev)
+    g = torch.empty(e, dtype=torch.float32, device=dev)
+    lib = _lib.load()
+    m = _matrix(logits)
+    with _on(dev) as stream:
+        nbytes = lib.fs_balance_workspace_bytes(ctypes.byref(m))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _raise(lib.fs_balance(ctypes.byref(m), _score_code(score), float(eps), int(n_iters),
+                              _ptr(load), _ptr(g_init), f.data_ptr(), g.data_ptr(), ws.data_ptr(),
+                              ws.numel(), stream))
+    return f, g
