@@ -447,6 +447,37 @@ FS_API fs_status fs_token_logprobs_grad(const fs_matrix* z, float eps, const voi
                                         int64_t ld_grad, fs_stream_t stream);
 
 /*
+ * fs_token_logprobs straight from states x (rows, dim) and an embedding w (cols, dim), both
+ * bf16 (FS_ERR_DTYPE otherwise), for z = x w^T, which is never stored: score tiles are formed on
+ * the tensor cores with float32 accumulation and folded into the rows' sums. logp, entropy, lse
+ * and stats mean the same, ids < 0 and ids >= cols too; there are no alternatives. x and w must
+ * be 16-byte aligned with row strides that are multiples of 8 elements (FS_ERR_ALIGNMENT
+ * otherwise); dim <= 2^20. Waits inside the kernels are bounded (2 s); if one expires the
+ * outputs are NaN. ws: the matching workspace size (0 for a shape that is not taken; it depends
+ * on the current device's SM count), 256-byte aligned.
+ */
+FS_API size_t fs_linear_logprobs_workspace_bytes(const fs_matrix* x, const fs_matrix* w);
+FS_API fs_status fs_linear_logprobs(const fs_matrix* x, const fs_matrix* w, float eps,
+                                    const void* ids, int32_t ids_64, float* logp, float* entropy,
+                                    float* lse, float* stats, void* ws, size_t ws_bytes,
+                                    fs_stream_t stream);
+
+/*
+ * Gradients of those: grad_x (rows, dim) = G w and grad_w (cols, dim) = G^T x, contiguous bf16,
+ * either may be NULL; G_ij = dL/dz_ij by the formula of fs_token_logprobs_grad, rounded to bf16
+ * as an operand of the products, which are summed in float32. The workspace holds G, at most
+ * 1 GiB of it at a time (more columns are done in chunks). An id >= cols makes grad_w NaN, and
+ * the row's grad_x.
+ */
+FS_API size_t fs_linear_logprobs_grad_workspace_bytes(const fs_matrix* x, const fs_matrix* w);
+FS_API fs_status fs_linear_logprobs_grad(const fs_matrix* x, const fs_matrix* w, float eps,
+                                         const void* ids, int32_t ids_64, const float* stats,
+                                         const float* entropy, const float* g_logp,
+                                         const float* g_entropy, const float* g_lse, void* grad_x,
+                                         void* grad_w, void* ws, size_t ws_bytes,
+                                         fs_stream_t stream);
+
+/*
  * Routing to experts. z (rows, experts <= FS_MAX_EXPERTS): a token's logits. With scores s =
  * softmax(z) or sigmoid(z) and c_j = s_j + bias_j (bias (experts) or NULL): of the `groups`
  * groups of consecutive experts (experts divisible by groups, groups <= 32) the top_groups with

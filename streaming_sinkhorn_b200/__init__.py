@@ -21,7 +21,8 @@ __all__ = ["potentials", "cost", "grad_x", "marginal_residual", "solve_host", "w
            "workspace_invalidate",
            "FsError", "timing_enable", "timing_reset", "timing_get", "launch_count",
            "screening_enable", "solve", "transport_apply", "hvp", "SamplesLoss",
-           "sinkhorn_divergence", "solve_multiscale", "token_logprobs", "route", "balance"]
+           "sinkhorn_divergence", "solve_multiscale", "token_logprobs",
+           "linear_logprobs", "route", "balance"]
 
 
 class FsError(RuntimeError):
@@ -431,4 +432,4 @@ def timing_get() -> dict:
 
 
 from .loss import SamplesLoss  # noqa: E402  (uses the functions above)
-from .rows import balance, route, token_logprobs  # noqa: E402
+from .rows import balance, linear_logprobs, route, token_logprobs  # noqa: E402

@@ -31,7 +31,8 @@ EXPORTS = (
     "fs_multiscale_workspace_bytes", "fs_solve_multiscale", "fs_workspace_invalidate",
     "fs_inject_error_word", "fs_check_bounded_wait", "fs_token_logprobs",
     "fs_token_logprobs_grad", "fs_route", "fs_route_grad", "fs_balance_workspace_bytes",
-    "fs_balance",
+    "fs_balance", "fs_linear_logprobs_workspace_bytes", "fs_linear_logprobs",
+    "fs_linear_logprobs_grad_workspace_bytes", "fs_linear_logprobs_grad",
 )
 
 # Limits of the row-softmax operators (include/fs.h).
@@ -178,13 +179,21 @@ def load():
     lib.fs_token_logprobs.argtypes = [M, f32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     lib.fs_token_logprobs_grad.argtypes = [M, f32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                            ctypes.c_int64, vp]
+    lib.fs_linear_logprobs_workspace_bytes.argtypes = [M, M]
+    lib.fs_linear_logprobs_workspace_bytes.restype = sz
+    lib.fs_linear_logprobs.argtypes = [M, M, f32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.fs_linear_logprobs_grad_workspace_bytes.argtypes = [M, M]
+    lib.fs_linear_logprobs_grad_workspace_bytes.restype = sz
+    lib.fs_linear_logprobs_grad.argtypes = [M, M, f32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                            vp]
     lib.fs_route.argtypes = [M, R, vp, vp, vp, vp]
     lib.fs_route_grad.argtypes = [M, R, vp, vp, vp, vp, vp]
     lib.fs_balance_workspace_bytes.argtypes = [M]
     lib.fs_balance_workspace_bytes.restype = sz
     lib.fs_balance.argtypes = [M, i32, f32, i32, vp, vp, vp, vp, vp, sz, vp]
     for fn in (lib.fs_token_logprobs, lib.fs_token_logprobs_grad, lib.fs_route,
-               lib.fs_route_grad, lib.fs_balance):
+               lib.fs_route_grad, lib.fs_balance, lib.fs_linear_logprobs,
+               lib.fs_linear_logprobs_grad):
         fn.restype = ctypes.c_int
     lib.fs_launch_count.argtypes = []
     lib.fs_launch_count.restype = ctypes.c_int64

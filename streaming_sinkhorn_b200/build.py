@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfs.so")
 OBJ = os.path.join(HERE, "_build")
-SOURCES = ["fs_api.cu", "fs_noalloc.cu", "fs_rows.cu"]
+SOURCES = ["fs_api.cu", "fs_noalloc.cu", "fs_rows.cu", "fs_linear.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,0 +1,390 @@
+// fs_linear.cu -- C ABI of fs_linear_logprobs and its gradient (include/fs.h): argument checks,
+// tensor maps, launch plans and launches. Nothing here waits for the device.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fs_host.h"
+#include "fs_linear.cuh"
+
+namespace fs {
+namespace {
+
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr size_t kHeader = 256;  // the error word
+// Most bytes of G in the workspace; a larger one is made in chunks of columns.
+constexpr int64_t kMaxG = int64_t(1) << 30;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+fs_status check_operand(const fs_matrix* m) {
+  if (!m) return FS_ERR_NULL;
+  // bf16 only: the gradient of a softmax falls below fp16's range, and fp32 operands have no
+  // tensor-core product that keeps their bits
+  if (m->dtype != FS_BF16) return FS_ERR_DTYPE;
+  if (m->rows < 0 || m->rows > kMaxInt - 512 || m->cols < 1 || m->cols > (1 << 20) ||
+      m->ld < m->cols || m->ld > (int64_t(1) << 36))
+    return FS_ERR_SHAPE;
+  if (m->rows > 0 && !m->data) return FS_ERR_NULL;
+  // TMA: 16-byte aligned base and row stride
+  if (!aligned(m->data, 16) || m->ld % 8 != 0) return FS_ERR_ALIGNMENT;
+  return FS_OK;
+}
+
+fs_status check_pair(const fs_matrix* x, const fs_matrix* w, float eps) {
+  fs_status s = check_operand(x);
+  if (s != FS_OK) return s;
+  if ((s = check_operand(w)) != FS_OK) return s;
+  if (x->cols != w->cols || w->rows < 1) return FS_ERR_SHAPE;
+  return std::isfinite(eps) && eps > 0.0f && std::isfinite(1.0f / eps) ? FS_OK : FS_ERR_EPS;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled by way of the runtime, so that the library needs no libcuda to load.
+fs_status encode_fn(EncodeFn* out) {
+  static std::atomic<void*> cached{nullptr};
+  void* p = cached.load(std::memory_order_acquire);
+  if (!p) {
+    cudaDriverEntryPointQueryResult q;
+    const fs_status s =
+        cuda_status(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q),
+                    "cudaGetDriverEntryPointByVersion");
+    if (s != FS_OK) return s;
+    if (q != cudaDriverEntryPointSuccess || !p) {
+      record_cuda_error("cuTensorMapEncodeTiled", cudaErrorSymbolNotFound);
+      return FS_ERR_CUDA;
+    }
+    cached.store(p, std::memory_order_release);
+  }
+  *out = reinterpret_cast<EncodeFn>(p);
+  return FS_OK;
+}
+
+// A (rows, cols) bf16 matrix read in boxes of 64 columns (128 bytes, swizzled) x box_rows rows;
+// what lies outside reads as zero.
+fs_status make_map(CUtensorMap* map, const void* data, int64_t rows, int64_t cols, int64_t ld,
+                   int box_rows) {
+  EncodeFn fn;
+  const fs_status s = encode_fn(&fn);
+  if (s != FS_OK) return s;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t step[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(data), dims,
+                        strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    record_cuda_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
+    return FS_ERR_CUDA;
+  }
+  return FS_OK;
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMap& b,
+                        const LinParams& P, int sms, cudaStream_t st) {
+  constexpr auto fn = linear_kernel<BN, A_MN, B_MN, EPI>;
+  static PerDeviceOnce once;
+  const fs_status s = once.run("cudaFuncSetAttribute", [&] {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(LinShape<BN>::SMEM));
+  });
+  if (s != FS_OK) return s;
+  const int64_t grid = std::min<int64_t>(P.units, sms);
+  return launch(what, fn, dim3(static_cast<unsigned>(grid)), kLinThreads, LinShape<BN>::SMEM, st,
+                1, a, b, P);
+}
+
+// The forward pass: tile width, column tiles of a unit, and how many units share a row block.
+struct ForwardPlan {
+  int bn;
+  int64_t m_blocks, n_blocks, per_unit, splits;
+  int64_t m_pad;
+  size_t off_given, total;
+};
+
+ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
+  ForwardPlan p{};
+  p.m_blocks = ceil_div(rows, kLinM);
+  // One row block reads w once and is bound by that read: narrow tiles spread it evenly over
+  // the SMs. More row blocks are bound by the products: wide tiles.
+  p.bn = p.m_blocks == 1 ? 128 : 256;
+  p.n_blocks = ceil_div(cols, p.bn);
+  // The split of the columns whose last wave is fullest; ties go to fewer parts.
+  double best = 0.0;
+  p.per_unit = 1;
+  for (int64_t per = p.n_blocks; per >= 1; --per) {
+    const int64_t units = p.m_blocks * ceil_div(p.n_blocks, per);
+    if (units > 16ll * sms && best > 0.0) break;
+    // tiles the busiest CTA takes, against an even share
+    const double even = static_cast<double>(p.m_blocks * p.n_blocks) / sms;
+    const double eff = even / static_cast<double>(ceil_div(units, sms) * per);
+    if (eff > best + 1e-3) {
+      best = eff;
+      p.per_unit = per;
+    }
+  }
+  p.splits = ceil_div(p.n_blocks, p.per_unit);
+  p.m_pad = p.m_blocks * kLinM;
+  p.off_given = kHeader + static_cast<size_t>(2 * p.splits * p.m_pad) * sizeof(float4);
+  p.total = round_up(p.off_given + static_cast<size_t>(p.m_pad) * 4, 256);
+  return p;
+}
+
+// The gradient: columns of a chunk of G, and the K splits of dx.
+struct BackwardPlan {
+  int64_t chunk, chunks, ld_g, splits;
+  size_t off_acc, total;
+};
+
+BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
+  BackwardPlan p{};
+  const int64_t cap = std::max<int64_t>(256, kMaxG / (2 * rows) / 256 * 256);
+  p.chunks = ceil_div(cols, cap);
+  p.chunk = std::min(round_up(ceil_div(cols, p.chunks), 256), cap);
+  p.chunks = ceil_div(cols, p.chunk);
+  p.ld_g = round_up(std::min(p.chunk, cols), 256);
+  // dx has few tiles and a long K: split K so that the last wave is full, counting the write
+  // and read of each split's fp32 partial sums (about 1 K step per 2^16 floats and SM)
+  const int64_t tiles = ceil_div(rows, kLinM) * ceil_div(dim, 256);
+  const int64_t k_steps = ceil_div(std::min(p.chunk, cols), kLinK);
+  double best = 0.0;
+  p.splits = 1;
+  for (int64_t s = 1; s <= 64 && s <= std::max<int64_t>(1, k_steps / 8); ++s) {
+    const double product =
+        static_cast<double>(ceil_div(tiles * s, sms)) * static_cast<double>(ceil_div(k_steps, s));
+    const double sums = s > 1 ? static_cast<double>(s) * rows * dim * 8.0 / 6.0e12 / 2.8e-7 : 0.0;
+    const double cost = product + sums;
+    if (s == 1 || cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
+  const size_t g = static_cast<size_t>(rows) * p.ld_g * 2;
+  p.off_acc = round_up(kHeader + g, 256);
+  const bool partial = p.splits > 1 || p.chunks > 1;
+  p.total = round_up(p.off_acc + (partial ? static_cast<size_t>(p.splits) * rows * dim * 4 : 0), 256);
+  return p;
+}
+
+bool shape_ok(const fs_matrix* x, const fs_matrix* w) {
+  return x && w && x->rows >= 0 && x->rows <= kMaxInt - 512 && w->rows >= 1 &&
+         w->rows <= kMaxInt - 512 && x->cols == w->cols && x->cols >= 1 && x->cols <= (1 << 20);
+}
+
+fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void* ids,
+                  int32_t ids_64, float* logp, float* entropy, float* lse, float* stats, void* ws,
+                  size_t ws_bytes, cudaStream_t st) {
+  fs_status s = check_pair(x, w, eps);
+  if (s != FS_OK) return s;
+  if (ids_64 != 0 && ids_64 != 1) return FS_ERR_OPTION;
+  if (x->rows == 0) return FS_OK;
+  if (!ids || !logp || !entropy) return FS_ERR_NULL;
+  if (!aligned(ids, ids_64 ? 8 : 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(stats, 8))
+    return FS_ERR_ALIGNMENT;
+  const int sms = current_sms();
+  const ForwardPlan p = forward_plan(x->rows, w->rows, sms);
+  if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  CUtensorMap ma, mb;
+  if ((s = make_map(&ma, x->data, x->rows, x->cols, x->ld, kLinM)) != FS_OK) return s;
+  if ((s = make_map(&mb, w->data, w->rows, w->cols, w->ld, p.bn)) != FS_OK) return s;
+  LinParams P{};
+  P.m = x->rows;
+  P.n = w->rows;
+  P.k_steps = static_cast<int32_t>(ceil_div(x->cols, kLinK));
+  P.m_blocks = static_cast<int32_t>(p.m_blocks);
+  P.n_blocks = static_cast<int32_t>(p.n_blocks);
+  P.n_per_unit = static_cast<int32_t>(p.per_unit);
+  P.k_splits = 1;
+  P.units = p.m_blocks * p.splits;
+  P.err = reinterpret_cast<unsigned*>(base);
+  P.inv_eps = 1.0f / eps;
+  P.ids = ids;
+  P.ids_wide = ids_64;
+  P.part = reinterpret_cast<float4*>(base + kHeader);
+  P.given = reinterpret_cast<float*>(base + p.off_given);
+  P.m_pad = p.m_pad;
+  P.cols = w->rows;
+  s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
+  if (s != FS_OK) return s;
+  s = p.bn == 128
+          ? launch_linear<128, false, false, kLinLse>("fs_linear_logprobs", ma, mb, P, sms, st)
+          : launch_linear<256, false, false, kLinLse>("fs_linear_logprobs", ma, mb, P, sms, st);
+  if (s != FS_OK) return s;
+  LinJoinParams J{};
+  J.part = P.part;
+  J.given = P.given;
+  J.parts = 2 * p.splits;
+  J.m = x->rows;
+  J.m_pad = p.m_pad;
+  J.cols = w->rows;
+  J.ids = ids;
+  J.ids_wide = ids_64;
+  J.inv_eps = P.inv_eps;
+  J.err = P.err;
+  J.logp = logp;
+  J.entropy = entropy;
+  J.lse = lse;
+  J.stats = reinterpret_cast<float2*>(stats);
+  return launch("fs_linear_logprobs (join)", linear_join_kernel,
+                dim3(static_cast<unsigned>(ceil_div(x->rows, 8))), 256, 0, st, 1, J);
+}
+
+fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void* ids,
+                   int32_t ids_64, const float* stats, const float* entropy, const float* g_logp,
+                   const float* g_entropy, const float* g_lse, void* grad_x, void* grad_w, void* ws,
+                   size_t ws_bytes, cudaStream_t st) {
+  fs_status s = check_pair(x, w, eps);
+  if (s != FS_OK) return s;
+  if (ids_64 != 0 && ids_64 != 1) return FS_ERR_OPTION;
+  if (!aligned(grad_x, 2) || !aligned(grad_w, 2)) return FS_ERR_ALIGNMENT;
+  const int64_t rows = x->rows, cols = w->rows, dim = x->cols;
+  if (rows == 0) {
+    if (!grad_w) return FS_OK;
+    return cuda_status(cudaMemsetAsync(grad_w, 0, static_cast<size_t>(cols) * dim * 2, st),
+                       "cudaMemsetAsync");
+  }
+  if (!ids || !stats || !entropy) return FS_ERR_NULL;
+  if (!aligned(ids, ids_64 ? 8 : 4) || !aligned(stats, 8) || !aligned(entropy, 4) ||
+      !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(g_lse, 4))
+    return FS_ERR_ALIGNMENT;
+  if (!grad_x && !grad_w) return FS_OK;
+  const int sms = current_sms();
+  const BackwardPlan p = backward_plan(rows, cols, dim, sms);
+  if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  unsigned* err = reinterpret_cast<unsigned*>(base);
+  __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(base + kHeader);
+  float* acc = reinterpret_cast<float*>(base + p.off_acc);
+  const bool partial = p.splits > 1 || p.chunks > 1;
+  __nv_bfloat16* gx = static_cast<__nv_bfloat16*>(grad_x);
+  __nv_bfloat16* gw = static_cast<__nv_bfloat16*>(grad_w);
+  s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
+  if (s != FS_OK) return s;
+  const __nv_bfloat16* wd = static_cast<const __nv_bfloat16*>(w->data);
+  for (int64_t c = 0; c < p.chunks; ++c) {
+    const int64_t col0 = c * p.chunk;
+    const int64_t n = std::min(p.chunk, cols - col0);
+    CUtensorMap ma, mb;
+    // G of the chunk: the scores again, and their gradient in the epilogue
+    if ((s = make_map(&ma, x->data, rows, dim, x->ld, kLinM)) != FS_OK) return s;
+    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256)) != FS_OK) return s;
+    LinParams P{};
+    P.m = rows;
+    P.n = n;
+    P.k_steps = static_cast<int32_t>(ceil_div(dim, kLinK));
+    P.m_blocks = static_cast<int32_t>(ceil_div(rows, kLinM));
+    P.n_blocks = static_cast<int32_t>(ceil_div(n, 256));
+    P.n_per_unit = 1;
+    P.k_splits = 1;
+    P.units = static_cast<int64_t>(P.m_blocks) * P.n_blocks;
+    P.err = err;
+    P.inv_eps = 1.0f / eps;
+    P.ids = ids;
+    P.ids_wide = ids_64;
+    P.col0 = col0;
+    P.cols = cols;
+    P.stats = reinterpret_cast<const float2*>(stats);
+    P.entropy = entropy;
+    P.g_logp = g_logp;
+    P.g_entropy = g_entropy;
+    P.g_lse = g_lse;
+    P.g_out = G;
+    P.ld_g = p.ld_g;
+    s = launch_linear<256, false, false, kLinScoreGrad>("fs_linear_logprobs_grad (scores)", ma, mb,
+                                                        P, sms, st);
+    if (s != FS_OK) return s;
+    if (gx) {  // dx = G w: K runs along G's rows and down w's
+      LinParams Q{};
+      if ((s = make_map(&ma, G, rows, n, p.ld_g, kLinM)) != FS_OK) return s;
+      if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 64)) != FS_OK) return s;
+      Q.m = rows;
+      Q.n = dim;
+      Q.k_steps = static_cast<int32_t>(ceil_div(n, kLinK));
+      Q.m_blocks = P.m_blocks;
+      Q.n_blocks = static_cast<int32_t>(ceil_div(dim, 256));
+      Q.k_splits = static_cast<int32_t>(p.splits);
+      Q.units = static_cast<int64_t>(Q.m_blocks) * Q.n_blocks * p.splits;
+      Q.err = err;
+      Q.out = partial ? nullptr : gx;
+      Q.acc = acc;
+      Q.add = c > 0;
+      Q.ld_out = dim;
+      s = launch_linear<256, false, true, kLinStore>("fs_linear_logprobs_grad (dx)", ma, mb, Q, sms,
+                                                     st);
+      if (s != FS_OK) return s;
+    }
+    if (gw) {  // dw = G^T x: K runs down both
+      LinParams Q{};
+      if ((s = make_map(&ma, G, rows, n, p.ld_g, 64)) != FS_OK) return s;
+      if ((s = make_map(&mb, x->data, rows, dim, x->ld, 64)) != FS_OK) return s;
+      Q.m = n;
+      Q.n = dim;
+      Q.k_steps = static_cast<int32_t>(ceil_div(rows, kLinK));
+      Q.m_blocks = static_cast<int32_t>(ceil_div(n, kLinM));
+      Q.n_blocks = static_cast<int32_t>(ceil_div(dim, 256));
+      Q.k_splits = 1;
+      Q.n_fast = 1;  // the tiles of one strip of G run together
+      Q.units = static_cast<int64_t>(Q.m_blocks) * Q.n_blocks;
+      Q.err = err;
+      Q.out = gw + col0 * dim;
+      Q.ld_out = dim;
+      s = launch_linear<256, true, true, kLinStore>("fs_linear_logprobs_grad (dw)", ma, mb, Q, sms,
+                                                    st);
+      if (s != FS_OK) return s;
+    }
+  }
+  if (gx && partial) {
+    const int64_t count = rows * dim;
+    s = launch("fs_linear_logprobs_grad (sum)", linear_reduce_kernel,
+               dim3(static_cast<unsigned>(ceil_div(count, 1024))), 256, 0, st, 1,
+               static_cast<const float*>(acc), static_cast<int>(p.splits), count, gx);
+    if (s != FS_OK) return s;
+  }
+  return launch("fs_linear_logprobs_grad (check)", linear_poison_kernel,
+                dim3(static_cast<unsigned>(sms)), 256, 0, st, 1, static_cast<const unsigned*>(err),
+                gx, gx ? rows * dim : int64_t(0), gw, gw ? cols * dim : int64_t(0));
+}
+
+}  // namespace
+}  // namespace fs
+
+extern "C" {
+
+size_t fs_linear_logprobs_workspace_bytes(const fs_matrix* x, const fs_matrix* w) {
+  if (!fs::shape_ok(x, w)) return 0;
+  return fs::forward_plan(std::max<int64_t>(x->rows, 1), w->rows, fs::current_sms()).total;
+}
+
+size_t fs_linear_logprobs_grad_workspace_bytes(const fs_matrix* x, const fs_matrix* w) {
+  if (!fs::shape_ok(x, w)) return 0;
+  return fs::backward_plan(std::max<int64_t>(x->rows, 1), w->rows, x->cols, fs::current_sms()).total;
+}
+
+fs_status fs_linear_logprobs(const fs_matrix* x, const fs_matrix* w, float eps, const void* ids,
+                             int32_t ids_64, float* logp, float* entropy, float* lse, float* stats,
+                             void* ws, size_t ws_bytes, fs_stream_t stream) {
+  return fs::forward(x, w, eps, ids, ids_64, logp, entropy, lse, stats, ws, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+fs_status fs_linear_logprobs_grad(const fs_matrix* x, const fs_matrix* w, float eps,
+                                  const void* ids, int32_t ids_64, const float* stats,
+                                  const float* entropy, const float* g_logp,
+                                  const float* g_entropy, const float* g_lse, void* grad_x,
+                                  void* grad_w, void* ws, size_t ws_bytes, fs_stream_t stream) {
+  return fs::backward(x, w, eps, ids, ids_64, stats, entropy, g_logp, g_entropy, g_lse, grad_x,
+                      grad_w, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

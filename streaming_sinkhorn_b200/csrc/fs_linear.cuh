@@ -1,0 +1,485 @@
+// fs_linear.cuh -- log probabilities of given tokens straight from states x (T, D) and an
+// embedding w (V, D), bf16, with z = x w^T never stored, and their gradients (sm_100a).
+//
+// Forward: one persistent pass forms 128-row score tiles on the tensor cores (products of
+// bf16 are exact in the fp32 accumulators) and its epilogue folds each tile into the rows'
+// running maximum, sum and entropy sum, as the pass over given scores does; a second kernel
+// joins the partial rows. Gradient: the scores are formed again, the epilogue turns each tile
+// into G_ij = dL/dz_ij in bf16 (at most 2^-8 relative in each term of the sums below: the
+// operands of the tensor cores; bf16 and not fp16, whose range ends above a small probability
+// over a batch's size), and two products finish it: dx = G w and dw = G^T x. G lives in the
+// workspace, in chunks of columns when all of it would not fit the cap.
+//
+// One kernel does all four: C = A B^T over 64-wide K steps, warp 0 streams both operands
+// through a ring with TMA (128-byte swizzle), warp 1 issues the MMAs into one of two TMEM
+// accumulators, eight warps run the epilogue of the other (lane quarter warp % 4, half of the
+// columns each). An operand whose K runs along its rows' elements (x, w of the scores; G of
+// dx) is K-major; one whose K runs down its rows (w of dx; G and x of dw) is read as it lies as
+// an MN-major operand, so nothing is transposed in memory.
+//
+// Every wait is bounded; a CTA that gives up sets the call's error word, and the outputs are
+// NaN.
+#pragma once
+
+#include <cuda.h>
+
+#include "fs_tcgen05.cuh"
+#include "fs_tokens.cuh"
+
+namespace fs {
+
+constexpr int kLinM = 128;       // rows of a tile (MMA M)
+constexpr int kLinK = 64;        // K step: 128 bytes of bf16, one swizzle span
+constexpr int kLinEpiWarps = 8;
+constexpr int kLinThreads = (4 + kLinEpiWarps) * 32;  // producer, MMA, TMEM owner, idle; epilogue
+constexpr uint32_t kLinRing = 192u * 1024u;           // bytes of the operand ring
+
+enum LinEpi : int { kLinLse = 0, kLinScoreGrad = 1, kLinStore = 2 };
+
+template <int BN>
+struct LinShape {
+  static constexpr uint32_t A_BYTES = kLinM * kLinK * 2;
+  static constexpr uint32_t B_BYTES = BN * kLinK * 2;
+  static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = static_cast<int>(kLinRing / STAGE);
+  static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
+  static constexpr uint32_t TMEM = 2 * BN;  // two accumulators
+};
+
+struct LinParams {
+  int64_t m, n;        // rows of C, columns of C that exist
+  int32_t k_steps;     // of the whole product
+  int32_t m_blocks, n_blocks;
+  int32_t n_per_unit;  // column tiles of a unit (kLinLse)
+  int32_t k_splits;    // parts of the K range (kLinStore)
+  int32_t n_fast;      // units go along n first
+  int64_t units;
+  unsigned* err;
+  float inv_eps;
+  const void* ids;
+  int32_t ids_wide;
+  // kLinLse
+  float4* part;    // (units' parts, m_pad): max, sum, entropy sum of a row
+  float* given;    // (m) score of the given token
+  int64_t m_pad;
+  // kLinScoreGrad
+  int64_t col0;    // first column of the chunk
+  int64_t cols;    // all columns (for the range of ids)
+  const float2* stats;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+  const float* g_lse;
+  __nv_bfloat16* g_out;
+  int64_t ld_g;
+  // kLinStore
+  __nv_bfloat16* out;  // bf16 output, or NULL: fp32 partial sums
+  float* acc;          // (k_splits, m, n)
+  int32_t add;         // add to acc (a later chunk)
+  int64_t ld_out;
+};
+
+// Shared-memory matrix descriptor, 128-byte swizzle, sm_100 version field. K-major: lbo unused,
+// sbo = 1024 (8 rows of 128 bytes). MN-major: a box is 64 K rows of 64 elements; lbo = its size
+// (the next 64 elements along M or N), sbo = 1024 (the next 8 K rows).
+__device__ __forceinline__ uint64_t lin_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16, bf16 operands, fp32 accumulators.
+__host__ __device__ constexpr uint32_t lin_idesc(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// What a unit covers: row block, column tiles [n0, n1), K steps [k0, k1), split.
+struct LinUnit {
+  int mb, n0, n1, k0, k1, split;
+};
+
+template <int EPI>
+__device__ __forceinline__ LinUnit lin_unit(const LinParams& P, int64_t u) {
+  LinUnit r;
+  if (EPI == kLinStore) {
+    const int64_t tiles = static_cast<int64_t>(P.m_blocks) * P.n_blocks;
+    r.split = static_cast<int>(u / tiles);
+    const int64_t t = u % tiles;
+    if (P.n_fast) {
+      r.mb = static_cast<int>(t / P.n_blocks);
+      r.n0 = static_cast<int>(t % P.n_blocks);
+    } else {
+      r.mb = static_cast<int>(t % P.m_blocks);
+      r.n0 = static_cast<int>(t / P.m_blocks);
+    }
+    r.n1 = r.n0 + 1;
+    r.k0 = static_cast<int>(static_cast<int64_t>(P.k_steps) * r.split / P.k_splits);
+    r.k1 = static_cast<int>(static_cast<int64_t>(P.k_steps) * (r.split + 1) / P.k_splits);
+  } else {
+    // neighbouring CTAs take other rows of the same columns: w is read from L2 but once
+    r.mb = static_cast<int>(u % P.m_blocks);
+    r.split = static_cast<int>(u / P.m_blocks);
+    r.n0 = r.split * P.n_per_unit;
+    r.n1 = min(r.n0 + P.n_per_unit, P.n_blocks);
+    r.k0 = 0;
+    r.k1 = P.k_steps;
+  }
+  return r;
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_b, const LinParams P) {
+  using S = LinShape<BN>;
+  extern __shared__ unsigned char lin_smem[];
+  __shared__ uint64_t full_bar[S::STAGES], free_bar[S::STAGES];
+  __shared__ uint64_t acc_bar[2], acc_free_bar[2];
+  __shared__ uint64_t fin_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  unsigned char* ring = lin_smem + ((1024u - (smem_u32(lin_smem) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  volatile int* abort = &abort_sh;
+
+  if (tid == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&free_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_bar[b], 1);
+      mbar_init(&acc_free_bar[b], kLinEpiWarps);
+    }
+    mbar_init(&fin_bar, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_base_sh)),
+                 "r"(S::TMEM));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t q = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+        const LinUnit w = lin_unit<EPI>(P, u);
+        for (int nb = w.n0; ok && nb < w.n1; ++nb) {
+          for (int k = w.k0; k < w.k1; ++k, ++q) {
+            const int s = static_cast<int>(q % S::STAGES);
+            const uint32_t round = static_cast<uint32_t>(q / S::STAGES);
+            if (round > 0 && !tc_wait(&free_bar[s], (round - 1) & 1u, abort)) {
+              ok = false;
+              break;
+            }
+            unsigned char* a = ring + static_cast<uint32_t>(s) * S::STAGE;
+            unsigned char* b = a + S::A_BYTES;
+            mbar_expect_tx(&full_bar[s], S::STAGE);
+            if constexpr (A_MN) {
+#pragma unroll
+              for (int i = 0; i < kLinM / 64; ++i)
+                tma_load_2d(a + i * 8192, &map_a, w.mb * kLinM + i * 64, k * kLinK, &full_bar[s]);
+            } else {
+              tma_load_2d(a, &map_a, k * kLinK, w.mb * kLinM, &full_bar[s]);
+            }
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i)
+                tma_load_2d(b + i * 8192, &map_b, nb * BN + i * 64, k * kLinK, &full_bar[s]);
+            } else {
+              tma_load_2d(b, &map_b, k * kLinK, nb * BN, &full_bar[s]);
+            }
+          }
+        }
+      }
+      if (*abort)  // the copies in flight land before the CTA's shared memory goes
+        for (int64_t v = q > S::STAGES ? q - S::STAGES : 0; v < q; ++v)
+          (void)mbar_wait_bounded(&full_bar[v % S::STAGES],
+                                  static_cast<uint32_t>(v / S::STAGES) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = lin_idesc(kLinM, BN, A_MN, B_MN);
+      int64_t q = 0;
+      uint32_t t = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+        const LinUnit w = lin_unit<EPI>(P, u);
+        for (int nb = w.n0; ok && nb < w.n1; ++nb, ++t) {
+          const uint32_t b = t & 1u;
+          if (t >= 2 && !tc_wait(&acc_free_bar[b], ((t >> 1) - 1) & 1u, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int k = w.k0; k < w.k1; ++k, ++q) {
+            const int s = static_cast<int>(q % S::STAGES);
+            if (!tc_wait(&full_bar[s], static_cast<uint32_t>(q / S::STAGES) & 1u, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(ring + static_cast<uint32_t>(s) * S::STAGE);
+            const uint32_t b0 = a0 + S::A_BYTES;
+#pragma unroll
+            for (int i = 0; i < kLinK / 16; ++i) {
+              // 16 elements of K: 32 bytes along a K-major row, 16 rows of an MN-major box
+              const uint64_t da = lin_desc(a0 + i * (A_MN ? 2048u : 32u), A_MN ? 8192u : 16u);
+              const uint64_t db = lin_desc(b0 + i * (B_MN ? 2048u : 32u), B_MN ? 8192u : 16u);
+              tc_mma_f16(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
+            }
+            tc_commit(&free_bar[s]);
+          }
+          if (ok) tc_commit(&acc_bar[b]);
+        }
+      }
+      // every MMA issued has completed once fin_bar fires: TMEM is never released under one
+      tc_commit(&fin_bar);
+      (void)mbar_wait_bounded(&fin_bar, 0);
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, grp = (warp - 4) >> 2;
+    constexpr int GC = BN / 2;  // columns of this warp's half
+    const int r = quarter * 32 + lane;
+    const float k2 = P.inv_eps * kLog2e;
+    uint32_t t = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+      const LinUnit w = lin_unit<EPI>(P, u);
+      const int64_t row = static_cast<int64_t>(w.mb) * kLinM + r;
+      const bool live = row < P.m;
+      // per row of the unit
+      TokenSum sum = {-INFINITY, 0.0f, 0.0f};
+      int64_t id = -1;
+      TokenRow tr = {0.0f, 0.0f, 0.0f, 0.0f};
+      float H = 0.0f, hot = 0.0f;
+      bool zero = true;
+      if (EPI != kLinStore && live) id = ld_id(P.ids, row, P.ids_wide != 0);
+      if (EPI == kLinScoreGrad && live && id >= 0) {
+        const float2 st = P.stats[row];
+        float gl = P.g_logp ? P.g_logp[row] : 0.0f;
+        if (id >= P.cols) gl = __int_as_float(0x7FC00000);
+        zero = false;
+        tr.m = st.x;
+        tr.log2_l = st.y * kLog2e;
+        tr.ge = P.g_entropy ? P.g_entropy[row] * P.inv_eps : 0.0f;
+        tr.c = ((P.g_lse ? P.g_lse[row] : 0.0f) - gl) * P.inv_eps;
+        hot = gl * P.inv_eps;
+        H = P.entropy[row];
+      }
+      for (int nb = w.n0; nb < w.n1; ++nb, ++t) {
+        const uint32_t b = t & 1u;
+        if (!tc_wait(&acc_bar[b], (t >> 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + grp * GC;
+        const int64_t c0 = static_cast<int64_t>(nb) * BN + grp * GC;
+        // split 0 .. of a K range that is empty leaves no MMA: its sum is zero
+        const bool none = EPI == kLinStore && w.k1 == w.k0;
+#pragma unroll 1
+        for (int c = 0; c < GC; c += 32) {
+          float v[32];
+          tc_ld32_nowait(base + c, v);
+          tc_wait_ld();
+          const int64_t col = c0 + c;
+          if constexpr (EPI == kLinLse) {
+            if (col + 32 > P.n) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col + j >= P.n) v[j] = -INFINITY;
+            }
+            const int64_t at = id - col;
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+              float z = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (at == j) z = v[j];
+              if (at >= 0 && at < 32 && id < P.n) P.given[row] = z;
+            }
+            float mx = fmaxf(v[0], v[1]);
+#pragma unroll
+            for (int j = 2; j < 32; j += 2) mx = max3(mx, v[j], v[j + 1]);
+            token_add<32>(sum, v, mx, k2);
+          } else if constexpr (EPI == kLinScoreGrad) {
+            const int64_t at = id - P.col0 - col;
+            if (live && col < P.n) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : token_dscore(tr, v[j], k2, H);
+              if (at >= 0 && at < 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (at == j) v[j] += hot;
+              }
+              // (columns past the last one fall into the row's padding)
+              uint4* o = reinterpret_cast<uint4*>(P.g_out + row * P.ld_g + col);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[j] = Elem<__nv_bfloat16>::pack(v + 8 * j);
+            }
+          } else {
+            if (live && col < P.n) {
+              if (none) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+              }
+              if (P.out) {
+                __nv_bfloat16* o = P.out + row * P.ld_out + col;
+                if (col + 32 <= P.n && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<uint4*>(o)[j] = Elem<__nv_bfloat16>::pack(v + 8 * j);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (col + j < P.n) o[j] = __float2bfloat16_rn(v[j]);
+                }
+              } else {
+                float* o = P.acc + (static_cast<int64_t>(w.split) * P.m + row) * P.n + col;
+                if (col + 32 <= P.n && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    float4* o4 = reinterpret_cast<float4*>(o) + j;
+                    float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    if (P.add) {
+                      const float4 y = *o4;
+                      x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+                    }
+                    *o4 = x;
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (col + j < P.n) o[j] = P.add ? o[j] + v[j] : v[j];
+                }
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_free_bar[b]);
+      }
+      if (EPI == kLinLse && ok)
+        P.part[(static_cast<int64_t>(w.split) * 2 + grp) * P.m_pad + row] =
+            make_float4(sum.m, sum.l, sum.a, 0.0f);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (abort_sh && tid == 0) atomicOr(P.err, kErrTimeout);
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(S::TMEM));
+}
+
+// ---- joining the parts -------------------------------------------------------------------------
+
+struct LinJoinParams {
+  const float4* part;
+  const float* given;
+  int64_t parts, m, m_pad, cols;
+  const void* ids;
+  int32_t ids_wide;
+  float inv_eps;
+  const unsigned* err;
+  float* logp;
+  float* entropy;
+  float* lse;
+  float2* stats;
+};
+
+// One warp per row: the parts of all units in their order.
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= P.m) return;
+  const int64_t id = ld_id(P.ids, row, P.ids_wide != 0);
+  const float k2 = P.inv_eps * kLog2e;
+  TokenSum s = {-INFINITY, 0.0f, 0.0f};
+  for (int64_t q = lane; q < P.parts; q += 32) {
+    const float4 o = P.part[q * P.m_pad + row];
+    s = token_merge(s, TokenSum{o.x, o.y, o.z}, k2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    TokenSum q;
+    q.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+    q.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+    q.a = __shfl_xor_sync(0xffffffffu, s.a, o);
+    s = (lane & o) ? token_merge(q, s, k2) : token_merge(s, q, k2);
+  }
+  if (lane != 0) return;
+  const float nan = __int_as_float(0x7FC00000);
+  const bool bad = *P.err != 0u;
+  const float log_l = logf(s.l);
+  if (id < 0 && !bad) {
+    P.logp[row] = 0.0f;
+    P.entropy[row] = 0.0f;
+    if (P.lse) P.lse[row] = 0.0f;
+    if (P.stats) P.stats[row] = make_float2(0.0f, 0.0f);
+    return;
+  }
+  P.logp[row] = bad || id >= P.cols ? nan : (P.given[row] - s.m) * P.inv_eps - log_l;
+  P.entropy[row] = bad ? nan : log_l - s.a / s.l * kLn2;
+  if (P.lse) P.lse[row] = bad ? nan : s.m * P.inv_eps + log_l;
+  if (P.stats) P.stats[row] = bad ? make_float2(nan, nan) : make_float2(s.m, log_l);
+}
+
+// out = bf16 of the sum of the splits' fp32 partial products, in their order.
+__global__ void __launch_bounds__(256)
+    linear_reduce_kernel(const float* acc, int splits, int64_t count, __nv_bfloat16* out) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  float v[4];
+  const int left = count - i < 4 ? static_cast<int>(count - i) : 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    const float* p = acc + s * count + i;
+    if (left == 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+    } else {
+      for (int j = 0; j < left; ++j) v[j] += p[j];
+    }
+  }
+  for (int j = 0; j < left; ++j) out[i + j] = __float2bfloat16_rn(v[j]);
+}
+
+// After a wait that expired: NaN in place of the gradients.
+__global__ void __launch_bounds__(256)
+    linear_poison_kernel(const unsigned* err, __nv_bfloat16* a, int64_t na, __nv_bfloat16* b,
+                         int64_t nb) {
+  if (*err == 0u) return;
+  const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7FC00000));
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < na; i += step) a[i] = nan;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < nb; i += step) b[i] = nan;
+}
+
+}  // namespace fs

@@ -40,6 +40,7 @@
 
 #include <cuda_fp16.h>
 #include "fs_kernels.cuh"
+#include "fs_tcgen05.cuh"
 
 namespace fs {
 
@@ -100,29 +101,6 @@ __host__ __device__ constexpr uint32_t tc_instr_desc(int M, int N, bool b_mn = f
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
 // The score tile of one 128-row block against one 128-key tile: three MMAs per 16-wide
 // K-step (hi.hi, lo.hi, hi.lo) into the accumulator at tmem_d. a0 and b0 are the
 // shared-memory addresses of the row and key images ([hi | lo], K-major).
@@ -145,38 +123,6 @@ __device__ __forceinline__ void tc_issue_scores(uint32_t tmem_d, uint32_t a0, ui
   }
 }
 
-// 32 consecutive fp32 columns of this thread's TMEM lane; the caller waits (tcgen05.wait::ld).
-__device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-}
-
-// 8 consecutive fp32 columns of this thread's TMEM lane; the caller waits.
-__device__ __forceinline__ void tc_ld8_nowait(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
-}
-
-__device__ __forceinline__ void tc_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 struct TcParams {
   const unsigned char* row_img;  // query cloud's image, tiles of 128 points
   const unsigned char* key_img;  // streamed cloud's image
@@ -187,30 +133,6 @@ struct TcParams {
   float c2;                      // 2 kappa / s^2: scale of the MMA result
   int32_t kc;                    // wide images (d > 64): 64-coordinate chunks per point
 };
-
-// Waits for phase `parity` of `bar`, giving up after kWaitLimitNs or as soon as another
-// role of the CTA has raised `abort`. Between checks the thread sleeps in the barrier wait
-// (up to 2 us per try), and the abort flag and the clock are read only every 16th try, so
-// waiting warps leave the shared-memory and special-function issue queues to the warps
-// that are computing.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (uint32_t k = 1;; ++k) {
-    if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
-    if ((k & 15u) == 0u) {
-      if (*abort) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // ---- epilogue pieces shared by the tensor-core kernels ------------------------------------
 

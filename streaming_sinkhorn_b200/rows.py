@@ -1,5 +1,6 @@
-"""Row-softmax operators on a given score matrix: log probabilities of given tokens, routing to
-experts, and the Sinkhorn bias that balances the experts' load.
+"""Row-softmax operators: log probabilities of given tokens, from a given score matrix or straight
+from states and an embedding, routing to experts, and the Sinkhorn bias that balances the
+experts' load.
 
 Only argument marshalling happens here: every number comes from the C ABI. Unlike the solves,
 these calls are asynchronous (they enqueue on the current stream of the data's device and
@@ -21,6 +22,14 @@ class TokenLogprobs(NamedTuple):
     lse: Any
     top_logprobs: Any
     top_ids: Any
+
+
+class LinearLogprobs(NamedTuple):
+    """Result of linear_logprobs: float32 tensors (T,)."""
+
+    logprobs: Any
+    entropy: Any
+    lse: Any
 
 
 class Routing(NamedTuple):
@@ -76,14 +85,15 @@ def _rows_of(t, name):
     _dtype_code(t.dtype, name)
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.stride(1) != 1 or t.stride(0) < t.shape[1]:
-        # (a single column or row may carry any stride: it is laid out anew too)
+    if (t.stride(1) != 1 and t.shape[1] > 1) or (t.stride(0) < t.shape[1] and t.shape[0] > 1):
         t = t.clone(memory_format=torch.contiguous_format)
     return t
 
 
 def _matrix(t):
-    return _lib.fs_matrix(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]),
+    n, c = t.shape
+    # (the stride of a single row is never used: any that the library takes will do)
+    return _lib.fs_matrix(t.data_ptr(), n, c, t.stride(0) if n > 1 else -(-c // 8) * 8,
                           _dtype_codes[t.dtype])
 
 
@@ -138,6 +148,7 @@ class _Functions:
     torch)."""
 
     token = None
+    linear = None
     routing = None
 
     @classmethod
@@ -174,6 +185,43 @@ class _Functions:
 
             cls.token = TokenLogprobsFunction
         return cls.token
+
+    @classmethod
+    def get_linear(cls):
+        if cls.linear is None:
+            torch = _torch()
+            from torch.autograd.function import once_differentiable
+
+            class LinearLogprobsFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, w, ids, eps):
+                    logp, entropy, lse, st = _linear_forward(x, w, ids, eps, True)
+                    ctx.save_for_backward(x, w, ids, entropy, st)
+                    ctx.eps = eps
+                    ctx.set_materialize_grads(False)
+                    return logp, entropy, lse
+
+                @staticmethod
+                @once_differentiable
+                def backward(ctx, g_logp, g_entropy, g_lse):
+                    x, w, ids, entropy, st = ctx.saved_tensors
+                    gx, gw = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
+                              for t, need in zip((x, w), ctx.needs_input_grad))
+                    lib = _lib.load()
+                    mx, mw = ctypes.byref(_matrix(x)), ctypes.byref(_matrix(w))
+                    keep = []
+                    with _on(x.device) as stream:
+                        ws = torch.empty(lib.fs_linear_logprobs_grad_workspace_bytes(mx, mw),
+                                         dtype=torch.uint8, device=x.device)
+                        _raise(lib.fs_linear_logprobs_grad(
+                            mx, mw, ctx.eps, ids.data_ptr(), int(ids.dtype == torch.int64),
+                            st.data_ptr(), entropy.data_ptr(), _grad_ptr(g_logp, keep),
+                            _grad_ptr(g_entropy, keep), _grad_ptr(g_lse, keep), _ptr(gx), _ptr(gw),
+                            ws.data_ptr(), ws.numel(), stream))
+                    return gx, gw, None, None
+
+            cls.linear = LinearLogprobsFunction
+        return cls.linear
 
     @classmethod
     def get_routing(cls):
@@ -235,6 +283,63 @@ def token_logprobs(logits, ids, *, eps: float = 1.0, top: int = 0) -> TokenLogpr
     if _needs_grad(logits):
         return TokenLogprobs(*_Functions.get_token().apply(logits, ids, eps, top))
     return TokenLogprobs(*_token_forward(logits, ids, eps, top, False)[:5])
+
+
+# ---- the same from states and an embedding ---------------------------------------------------
+
+def _linear_forward(x, w, ids, eps, stats):
+    torch = _torch()
+    n, dev = x.shape[0], x.device
+    f32 = torch.float32
+    logp = torch.empty(n, dtype=f32, device=dev)
+    entropy = torch.empty(n, dtype=f32, device=dev)
+    lse = torch.empty(n, dtype=f32, device=dev)
+    st = torch.empty((n, 2), dtype=f32, device=dev) if stats else None
+    lib = _lib.load()
+    mx, mw = ctypes.byref(_matrix(x)), ctypes.byref(_matrix(w))
+    with _on(dev) as stream:
+        ws = torch.empty(lib.fs_linear_logprobs_workspace_bytes(mx, mw), dtype=torch.uint8,
+                         device=dev)
+        _raise(lib.fs_linear_logprobs(mx, mw, eps, ids.data_ptr(), int(ids.dtype == torch.int64),
+                                      logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                                      _ptr(st), ws.data_ptr(), ws.numel(), stream))
+    return logp, entropy, lse, st
+
+
+def _operand(t, name):
+    """``t`` as an operand of the tensor-core products: 16-byte aligned rows (a copy with
+    padded rows where they are not)."""
+    torch = _torch()
+    t = _rows_of(t, name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} is {t.dtype}: only bfloat16 is supported")
+    if t.data_ptr() % 16 or (t.stride(0) % 8 and t.shape[0] > 1):
+        d = t.shape[1]
+        t = (torch.nn.functional.pad(t, (0, -d % 8))[:, :d] if d % 8 else
+             t.clone(memory_format=torch.contiguous_format))
+    return t
+
+
+def linear_logprobs(x, w, ids, *, eps: float = 1.0) -> LinearLogprobs:
+    """token_logprobs(x @ w.T, ids) without the scores ever stored (fs_linear_logprobs).
+
+    x: (T, D) states and w: (V, D) embedding, bfloat16, rows any stride apart (rows whose
+    addresses are not multiples of 16 bytes are copied first); ids and eps as in
+    token_logprobs. Scores are exact products summed in float32. Differentiable for x and w
+    through logprobs, entropy and lse; the scores' gradient is rounded to bfloat16 as an
+    operand of the two products.
+    """
+    x, w = _operand(x, "x"), _operand(w, "w")
+    torch = _torch()
+    if w.device != x.device:
+        raise ValueError(f"w is on {w.device}, expected {x.device}")
+    if w.shape[1] != x.shape[1] or w.shape[0] < 1:
+        raise ValueError(f"x has D={x.shape[1]} but w has shape {tuple(w.shape)}")
+    ids = _vector(ids, "ids", x.shape[0], x.device, (torch.int64, torch.int32))
+    eps = float(eps)
+    if _needs_grad(x, w):
+        return LinearLogprobs(*_Functions.get_linear().apply(x, w, ids, eps))
+    return LinearLogprobs(*_linear_forward(x, w, ids, eps, False)[:3])
 
 
 # ---- routing to experts ------------------------------------------------------------------------

@@ -168,3 +168,19 @@ def balance_ref(z, score, eps, n_iters, load=None, g_init=None):
         g = torch.where(cols, g, torch.zeros_like(g))
         g = torch.where(b > 0, g, torch.full_like(g, -math.inf))
     return eps * f, eps * g
+
+
+def linear_ref(x, w, ids, eps=1.0, **g):
+    """token_ref of z = x w^T with the gradients of x and w, and what bounds their errors: the
+    largest error of a score in fp32 accumulation (16 products a step, each sum off by at most
+    2^-23 of the absolute sum) and the absolute sums |G| |w|, |G|^T |x|."""
+    xd, wd = x.detach().cpu().double(), w.detach().cpu().double()
+    ref = token_ref(xd @ wd.t(), ids, eps, **g)
+    d = ref["grad"]
+    ref["grad_x"], ref["grad_w"] = d @ wd, d.t() @ xd
+    ref["abs_x"], ref["abs_w"] = d.abs() @ wd.abs(), d.abs().t() @ xd.abs()
+    # |G| with its terms apart: what an error of p alone moves
+    ref["size_x"] = ref["grad_size"] @ wd.abs()
+    ref["size_w"] = ref["grad_size"].t() @ xd.abs()
+    ref["dz"] = (x.shape[1] / 16 + 2) * 2 * U * float((xd.abs() @ wd.abs().t()).max()) / eps
+    return ref

@@ -184,6 +184,141 @@ def test_tokens_gradient_against_differences():
         assert float((g.cpu().double() * d).sum()) == pytest.approx(num, abs=1e-4)
 
 
+# ---- log probabilities from states and an embedding ------------------------------------------
+
+def check_linear(x, w, ids, eps=1.0, seed=0):
+    n, v = x.shape[0], w.shape[0]
+    x, w = x.detach().requires_grad_(True), w.detach().requires_grad_(True)
+    out = fs.linear_logprobs(x, w, ids, eps=eps)
+    g = {"g_logp": rand(n, seed=seed + 2), "g_entropy": rand(n, seed=seed + 3),
+         "g_lse": rand(n, seed=seed + 4)}
+    gx, gw = torch.autograd.grad(list(out), (x, w), list(g.values()))
+    ref = ru.linear_ref(x, w, ids, eps, **g)
+    t_lse, t_logp, t_h = ru.token_tol(ref, v, ref["logprobs"])
+    dz = ref["dz"]
+    ru.assert_near(out.logprobs, ref["logprobs"], t_logp + 2 * dz, "logprobs")
+    ru.assert_near(out.entropy, ref["entropy"], t_h + 2 * dz * (1 + ref["entropy"]), "entropy")
+    ru.assert_near(out.lse, ref["lse"], t_lse + dz + 3 * ru.U * ref["lse"].abs(), "lse")
+    # G is rounded to bf16 (half a step, finfo.eps / 2 = 2^-8 of each term), p is off by its argument's error, the sums run in
+    # fp32 over the tensor cores' 16-term steps, and the result is rounded once
+    rel_p = 2 * (float(t_lse.max()) + 2 * dz + 64 * ru.U)
+    for got, name, k in ((gx, "x", v), (gw, "w", n)):
+        ref_g, size, terms = ref["grad_" + name], ref["size_" + name], ref["abs_" + name]
+        acc = (k / 16 + 2) * 2 * ru.U
+        tol = ((2.0 ** -8 + acc) * terms + (rel_p + acc) * size) * 1.01 + \
+            ru.type_tol(ref_g, BF) * 1.01 + 1e-37
+        assert got.dtype == BF and got.shape == ref_g.shape
+        ru.assert_near(got, ref_g, tol, "grad_" + name)
+    return out
+
+
+@pytest.mark.parametrize("rows,cols,dim", [(1, 1, 8), (1, 300, 64), (5, 33, 16), (128, 256, 64),
+                                           (129, 257, 72), (300, 1000, 200), (2, 5000, 512),
+                                           (257, 3001, 96), (640, 2050, 328)])
+def test_linear_matches_float64(rows, cols, dim):
+    x, w = rand(rows, dim, seed=rows, dtype=BF, scale=1.0), rand(cols, dim, seed=cols + 1, dtype=BF,
+                                                                  scale=2.0 / math.sqrt(dim))
+    ids = randint(rows, cols, seed=dim)
+    if rows > 4:
+        ids[1::5] = -100
+    check_linear(x, w, ids, seed=rows)
+
+
+def test_linear_layouts_and_temperature():
+    x, w = rand(40, 130, seed=1, dtype=BF, scale=1.0), rand(70, 130, seed=2, dtype=BF, scale=0.2)
+    ids = randint(40, 70, dtype=torch.int32)
+    for d0, d in ((0, 128), (2, 64), (8, 100), (1, 77), (0, 1), (0, 130)):
+        check_linear(x[:, d0:d0 + d], w[:, d0:d0 + d], ids, eps=0.7)
+    check_linear(x[::3], w.t().contiguous().t(), ids[:14])
+
+
+def test_linear_agrees_with_the_scores_form():
+    x, w = rand(200, 64, seed=3, dtype=BF, scale=1.0), rand(900, 64, seed=4, dtype=BF, scale=0.3)
+    ids = randint(200, 900)
+    a, b = fs.linear_logprobs(x, w, ids), fs.token_logprobs(x.float() @ w.float().t(), ids)
+    for s, t in zip(a, b):
+        assert float((s - t).abs().max()) < 1e-4  # two orders of fp32 sums of 64 products
+
+
+def test_linear_one_gradient_only_and_no_rows():
+    x, w = rand(30, 32, seed=5, dtype=BF), rand(90, 32, seed=6, dtype=BF)
+    ids = randint(30, 90)
+    both = [t.clone().requires_grad_(True) for t in (x, w)]
+    gx, gw = torch.autograd.grad(fs.linear_logprobs(*both, ids).logprobs.sum(), both)
+    only = x.clone().requires_grad_(True)
+    assert torch.equal(torch.autograd.grad(fs.linear_logprobs(only, w, ids).logprobs.sum(), only)[0], gx)
+    only = w.clone().requires_grad_(True)
+    assert torch.equal(torch.autograd.grad(fs.linear_logprobs(x, only, ids).logprobs.sum(), only)[0], gw)
+    e = torch.empty(0, 32, dtype=BF, device="cuda").requires_grad_(True)
+    out = fs.linear_logprobs(e, both[1], torch.zeros(0, dtype=torch.long, device="cuda"))
+    gx, gw = torch.autograd.grad(out.logprobs.sum(), (e, both[1]))
+    assert gx.shape == (0, 32) and float(gw.abs().max()) == 0.0
+
+
+def test_linear_ids_out_of_range_and_nan():
+    x, w = rand(150, 32, seed=7, dtype=BF), rand(300, 32, seed=8, dtype=BF)
+    ids = randint(150, 300)
+    ids[3] = 300
+    x[5, 0] = math.nan
+    x.requires_grad_(True)
+    out = fs.linear_logprobs(x, w, ids)
+    bad = torch.isnan(out.logprobs).nonzero().flatten().tolist()
+    assert bad == [3, 5] and torch.isnan(out.entropy).nonzero().flatten().tolist() == [5]
+    (g,) = torch.autograd.grad(out.logprobs.sum(), x)
+    assert torch.isnan(g).any(1).nonzero().flatten().tolist() == [3, 5]
+
+
+def test_linear_gradient_in_chunks_of_columns():
+    # more than 1 GiB of G: two chunks, the states' gradient added over both
+    rows, cols, dim = 8200, 70000, 16
+    x, w = rand(rows, dim, seed=9, dtype=BF, scale=1.0), rand(cols, dim, seed=10, dtype=BF, scale=0.3)
+    ids = randint(rows, cols)
+    leaves = [t.requires_grad_(True) for t in (x, w)]
+    out = fs.linear_logprobs(x, w, ids)
+    gx, gw = torch.autograd.grad(out.logprobs.sum(), leaves)
+    xd, wd = x.detach().double(), w.detach().double()
+    d = -torch.softmax(xd @ wd.t(), 1)
+    d[torch.arange(rows), ids] += 1.0
+    for got, ref, terms in ((gx, d @ wd, d.abs() @ wd.abs()), (gw, d.t() @ xd, d.abs().t() @ xd.abs())):
+        # 2^-8 from G, 2^-8 from the result, p's own error and the fp32 sums within 2^-10 more
+        assert bool(((got.double() - ref).abs() <= 2.0 ** -8 * 1.25 * terms + 2.0 ** -8 * ref.abs()).all())
+
+
+def test_linear_in_a_graph_and_on_two_streams():
+    x, w = rand(70, 64, seed=11, dtype=BF, scale=1.0), rand(4000, 64, seed=12, dtype=BF, scale=0.3)
+    ids = randint(70, 4000)
+    x.requires_grad_(True)
+    w.requires_grad_(True)
+
+    def step():
+        out = fs.linear_logprobs(x, w, ids)
+        return (*out, *torch.autograd.grad(out.logprobs, (x, w), torch.ones_like(out.logprobs)))
+
+    want = [t.detach().clone() for t in step()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(2):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(step())
+    torch.cuda.synchronize()
+    s = streams[0]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    got.append(out)
+    for g in got:
+        for a, b in zip(want, g):
+            assert torch.equal(a, b)
+
+
 # ---- routing -----------------------------------------------------------------------------------
 
 def check_route(z, k, grads=True, seed=0, **kw):

@@ -139,6 +139,62 @@ def test_balance_arguments():
     assert balance(ws_bytes=need - 1) == "FS_ERR_WORKSPACE"
 
 
+def linear(x=mat(dtype=2), w=mat(dtype=2, rows=100), eps=1.0, ids=FAKE, ids_64=1, logp=FAKE,
+           entropy=FAKE, lse=None, stats=None, ws=FAKE, ws_bytes=BIG):
+    ref = lambda m: None if m is None else ctypes.byref(m)  # noqa: E731
+    return st(_lib.load().fs_linear_logprobs(ref(x), ref(w), eps, ids, ids_64, logp, entropy, lse,
+                                             stats, ws, ws_bytes, None))
+
+
+def linear_grad(x=mat(dtype=2), w=mat(dtype=2, rows=100), eps=1.0, ids=FAKE, ids_64=1, stats=FAKE,
+                entropy=FAKE, g=None, gx=FAKE, gw=FAKE, ws=FAKE, ws_bytes=BIG):
+    ref = lambda m: None if m is None else ctypes.byref(m)  # noqa: E731
+    return st(_lib.load().fs_linear_logprobs_grad(ref(x), ref(w), eps, ids, ids_64, stats, entropy,
+                                                  g, None, None, gx, gw, ws, ws_bytes, None))
+
+
+@pytest.mark.parametrize("z,expect", [
+    (None, "FS_ERR_NULL"), (mat(data=None, dtype=2), "FS_ERR_NULL"), (mat(dtype=0), "FS_ERR_DTYPE"),
+    (mat(dtype=1), "FS_ERR_DTYPE"), (mat(rows=-1, dtype=2), "FS_ERR_SHAPE"),
+    (mat(cols=0, dtype=2), "FS_ERR_SHAPE"), (mat(ld=60, dtype=2), "FS_ERR_SHAPE"),
+    (mat(ld=68, dtype=2), "FS_ERR_ALIGNMENT"), (mat(data=FAKE + 8, dtype=2), "FS_ERR_ALIGNMENT"),
+    (mat(cols=72, dtype=2), "FS_ERR_SHAPE"),  # not the other's dim
+])
+def test_bad_operands_of_the_linear_form(z, expect):
+    for call in (linear, linear_grad):
+        assert call(x=z) == expect
+        assert call(w=z) == expect
+
+
+def test_linear_arguments():
+    lib = _lib.load()
+    x, w = mat(dtype=2), mat(dtype=2, rows=100)
+    need = lib.fs_linear_logprobs_workspace_bytes(ctypes.byref(x), ctypes.byref(w))
+    need_g = lib.fs_linear_logprobs_grad_workspace_bytes(ctypes.byref(x), ctypes.byref(w))
+    assert need > 0 and need % 256 == 0 and need_g > 4 * 100 * 2 and need_g % 256 == 0
+    other = mat(cols=72, dtype=2)
+    assert lib.fs_linear_logprobs_workspace_bytes(ctypes.byref(x), ctypes.byref(other)) == 0
+    assert lib.fs_linear_logprobs_grad_workspace_bytes(None, ctypes.byref(w)) == 0
+    # the gradient keeps at most 1 GiB of G, plus the sums of dx
+    big = [mat(rows=r, cols=1024, dtype=2) for r in (8192, 262144)]
+    assert lib.fs_linear_logprobs_grad_workspace_bytes(*map(ctypes.byref, big)) < 2 << 30
+    assert linear(w=mat(dtype=2, rows=0)) == "FS_ERR_SHAPE"
+    for eps in (0.0, NAN, INF, -2.0):
+        assert linear(eps=eps) == "FS_ERR_EPS" and linear_grad(eps=eps) == "FS_ERR_EPS"
+    assert linear(ids_64=2) == "FS_ERR_OPTION" and linear_grad(ids_64=-1) == "FS_ERR_OPTION"
+    for name in ("ids", "logp", "entropy"):
+        assert linear(**{name: None}) == "FS_ERR_NULL"
+    for name in ("ids", "stats", "entropy"):
+        assert linear_grad(**{name: None}) == "FS_ERR_NULL"
+    assert linear(stats=FAKE + 4) == "FS_ERR_ALIGNMENT"
+    assert linear_grad(g=FAKE + 2) == "FS_ERR_ALIGNMENT"
+    assert linear_grad(gx=FAKE + 1) == "FS_ERR_ALIGNMENT"
+    assert linear_grad(gx=None, gw=None) == "FS_OK"
+    for call, size in ((linear, need), (linear_grad, need_g)):
+        assert call(ws=None) == "FS_ERR_WORKSPACE" and call(ws=FAKE + 64) == "FS_ERR_WORKSPACE"
+        assert call(ws_bytes=size - 1) == "FS_ERR_WORKSPACE"
+
+
 def test_python_binding_refuses():
     z = torch.zeros(4, 16)
     ids = torch.zeros(4, dtype=torch.long)
@@ -154,3 +210,6 @@ def test_python_binding_refuses():
             call(z[0])
         with pytest.raises(TypeError, match="Tensor"):
             call(z.numpy())
+    for bad in (z, z.half()):
+        with pytest.raises(ValueError, match="CUDA"):
+            fs.linear_logprobs(bad, bad, ids)
