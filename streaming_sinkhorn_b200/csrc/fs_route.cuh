@@ -46,15 +46,6 @@ struct RouteParams {
   int32_t* load;  // zeroed before the launch, or NULL
 };
 
-// Whole number that orders like c; 0 is below every number and stands for a closed expert.
-__device__ __forceinline__ uint32_t route_key(float c) {
-  const uint32_t b = __float_as_uint(c + 0.0f);  // -0 counts as 0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float route_unkey(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
 __device__ __forceinline__ float warp_maxf(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
       // closed: a logit or a bias of -inf
       const bool open = v[i] != -INFINITY && c != -INFINITY;
       bad |= open && c != c;
-      key[i] = open ? route_key(c) : 0u;
+      key[i] = open ? order_key(c) : 0u;
     }
     if (__any_sync(0xffffffffu, bad)) {
       route_write(P, row, lane, -1, __int_as_float(0x7FC00000));
@@ -225,7 +216,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     if (P.groups > 1) {
 #pragma unroll
       for (int i = 0; i < NL; ++i)
-        if (lane + 32 * i < E) c32[lane + 32 * i] = key[i] ? route_unkey(key[i]) : -INFINITY;
+        if (lane + 32 * i < E) c32[lane + 32 * i] = key[i] ? order_unkey(key[i]) : -INFINITY;
       __syncwarp();
       // the two largest of each group: `lanes` neighbouring lanes scan one group
       int lanes = 32;
@@ -303,7 +294,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
       zr = Elem<T>::to_f(z[mine]);
       s = route_score(zr, P.score, m, inv);
       br = P.bias ? P.bias[mine] : 0.0f;
-      c = route_unkey(mine_key);
+      c = order_unkey(mine_key);
       err = route_err(zr, s, c, P.score, m);
     }
     const int nmine = __shfl_down_sync(0xffffffffu, mine, 1);

@@ -92,6 +92,16 @@ __device__ __forceinline__ int64_t ld_id(const void* ids, int64_t i, bool wide) 
   return wide ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
 }
 
+// Whole number that orders like v (not for NaN); -0 counts as 0. Above 0, so 0 can stand for
+// "none".
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_unkey(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
 // Where the 16-byte vectors of a row begin and how many there are: elements [0, head) and
 // [head + nvec * kVec, cols) are read one by one.
 template <typename T>

@@ -10,9 +10,9 @@
 // instructions per score stay below it (4096 x 65536 bf16, forward: see kTokenThreads).
 //
 // Order of alternatives: larger z first, equal z by the lower index. Each warp keeps its best
-// `top` (value, index) pairs sorted across its lanes and looks at a vector's elements only
-// where the vector's maximum reaches the last kept value: about top * ln(n / top) insertions
-// over n scores in random order.
+// (value, index) pairs as sorted whole numbers across its lanes, and the CTA the largest of the
+// warps' last kept pairs: a round of vectors is looked at one by one only where its maximum
+// reaches that bar, which after the first round happens about top * ln(n / n0) times a row.
 //
 // A row is read by one CTA, or by a cluster of up to 8 when there are few rows (a decoding
 // step), whose partial results meet in the first CTA through distributed shared memory: one
@@ -105,69 +105,157 @@ __device__ __forceinline__ void token_add(TokenSum& s, const float* z, float zma
   }
 }
 
-// A warp's best pairs, lane i holding the i-th, and the last kept one in every lane.
-struct TokenBest {
-  float v;
-  int i;
-  float thr_v;
-  int thr_i;
-};
+// A score and its column as one whole number: larger score first, then the lower column. 0 is
+// below all of them and stands for none.
+__device__ __forceinline__ u64 token_key(float v, int i) {
+  return (static_cast<u64>(order_key(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ float token_key_value(u64 k) {
+  return order_unkey(static_cast<uint32_t>(k >> 32));
+}
+__device__ __forceinline__ int token_key_index(u64 k) {
+  return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+}
+__device__ __forceinline__ u64 max_u64(u64 a, u64 b) { return a > b ? a : b; }
+__device__ __forceinline__ u64 min_u64(u64 a, u64 b) { return a < b ? a : b; }
 
-__device__ __forceinline__ bool token_better(float v, int i, float w, int j) {
-  return v > w || (v == w && i < j);
+// The warp's keys, one per lane, sorted: the largest in lane 0 (bitonic, 15 exchanges).
+__device__ __forceinline__ u64 token_sort(u64 k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const u64 p = __shfl_xor_sync(0xffffffffu, k, o);
+      k = ((lane & o) == 0) == ((lane & size) == 0) ? max_u64(k, p) : min_u64(k, p);
+    }
+  return k;
 }
 
-// Inserts (v, i), the same in every lane; a pair behind the last kept one changes nothing.
-__device__ __forceinline__ void token_insert(TokenBest& b, float v, int i, int top, int lane) {
-  const int pos = __popc(__ballot_sync(0xffffffffu, token_better(b.v, b.i, v, i)));
-  if (pos >= top) return;
-  const float uv = __shfl_up_sync(0xffffffffu, b.v, 1);
-  const int ui = __shfl_up_sync(0xffffffffu, b.i, 1);
-  if (lane > pos) {
-    b.v = uv;
-    b.i = ui;
-  } else if (lane == pos) {
-    b.v = v;
-    b.i = i;
+// The 32 largest of two sorted lists, sorted: each lane keeps the larger of a's i-th and b's
+// i-th last, which leaves a bitonic sequence, and five exchanges sort it.
+__device__ __forceinline__ u64 token_join(u64 a, u64 b, int lane) {
+  a = max_u64(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 p = __shfl_xor_sync(0xffffffffu, a, o);
+    a = (lane & o) == 0 ? max_u64(a, p) : min_u64(a, p);
   }
-  b.thr_v = __shfl_sync(0xffffffffu, b.v, top - 1);
-  b.thr_i = __shfl_sync(0xffffffffu, b.i, top - 1);
+  return a;
 }
 
-// Offers one score per lane (a lane without one passes ok = false).
-__device__ __forceinline__ void token_offer(TokenBest& b, float v, int i, bool ok, int top,
-                                            int lane) {
-  unsigned c = __ballot_sync(0xffffffffu, ok && token_better(v, i, b.thr_v, b.thr_i));
+// Inserts key (the same in every lane) into the sorted list.
+__device__ __forceinline__ u64 token_insert(u64 list, u64 key, int lane) {
+  const int pos = __popc(__ballot_sync(0xffffffffu, list > key));
+  const u64 up = __shfl_up_sync(0xffffffffu, list, 1);
+  return lane > pos ? up : lane == pos ? key : list;
+}
+
+// Inserts the lanes' keys (0: none) that are above the list's last kept one.
+__device__ __forceinline__ u64 token_offer(u64 list, u64 key, int top, int lane) {
+  unsigned c = __ballot_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, list, top - 1));
   while (c) {
     const int src = __ffs(c) - 1;
     c &= c - 1;
-    token_insert(b, __shfl_sync(0xffffffffu, v, src), __shfl_sync(0xffffffffu, i, src), top, lane);
+    list = token_insert(list, __shfl_sync(0xffffffffu, key, src), lane);
   }
+  return list;
 }
 
-// The 16-byte word's element e (a loop variable), for the rare look at single elements.
-template <typename T>
-__device__ __forceinline__ float token_element(const uint4& r, int e) {
-  constexpr int per = 4 / sizeof(T);
-  const int q = e / per;
-  const uint32_t w = q == 0 ? r.x : q == 1 ? r.y : q == 2 ? r.z : r.w;
-  if constexpr (per == 1) {
-    return __uint_as_float(w);
-  } else {
-    const uint16_t h = static_cast<uint16_t>(w >> ((e & 1) * 16));
-    return Elem<T>::to_f(*reinterpret_cast<const T*>(&h));
-  }
-}
+// Candidates that a warp gathers from one round of vectors before it sorts them.
+constexpr int kTokenBuffer = 128;
 
 struct TokenShared {
   TokenSum sum[kTokenWarps];
-  float best_v[kTokenWarps][kTokenMaxTop];
-  int best_i[kTokenWarps][kTokenMaxTop];
+  u64 best[kTokenWarps][32];
+  u64 buffer[kTokenWarps][kTokenBuffer];
+  // the largest of the warps' last kept keys: nothing below it is among the row's best
+  u64 bar;
   // the CTA's result, read by the cluster's first CTA
   TokenSum total;
-  float total_v[kTokenMaxTop];
-  int total_i[kTokenMaxTop];
+  u64 total_best[32];
 };
+
+// Adds one round's vectors (f: U x V scores of this lane, the first of vector u at column
+// first + u * stride, n of them valid) to the warp's list. Gathers the scores above the bar in
+// shared memory, then inserts a few one by one or sorts and joins many at once. In the first
+// round the bar is raised beforehand: `top` lanes' maxima are at or above the top-th largest
+// of them, so whatever lies below that one is not among the row's best.
+template <typename T, int U>
+__device__ __forceinline__ u64 token_gather(u64 list, u64& bar, const float* f, const float* vmax,
+                                            float bm, int n, int first, int stride, int top,
+                                            const T* z, u64* buffer, u64* shared_bar, int lane) {
+  constexpr int V = Elem<T>::kVec;
+  float bar_v = token_key_value(bar);
+  int bar_i = token_key_index(bar);
+  if (bar == 0) {
+    bar_v = -INFINITY;
+    bar_i = 0x7FFFFFFF;
+    uint32_t mine = n > 0 && bm == bm ? order_key(bm) : 0u, t = 0u;
+    for (int r = 0; r < top; ++r) {
+      t = __reduce_max_sync(0xffffffffu, mine);
+      if (t == 0u) break;
+      // (equal maxima count one by one)
+      const unsigned at = __ballot_sync(0xffffffffu, mine == t);
+      if (lane == __ffs(at) - 1) mine = 0u;
+    }
+    if (t != 0u) bar_v = order_unkey(t);
+  }
+  int count = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n && vmax[u] >= bar_v) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = f[u * V + e];
+        count += v > bar_v || (v == bar_v && first + u * stride + e < bar_i);
+      }
+    }
+  int before = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int q = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += q;
+  }
+  const int total = __shfl_sync(0xffffffffu, before, 31);
+  if (total == 0) return list;
+  if (total <= kTokenBuffer) {
+    int at = before - count;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < n && vmax[u] >= bar_v) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float v = f[u * V + e];
+          const int i = first + u * stride + e;
+          if (v > bar_v || (v == bar_v && i < bar_i)) buffer[at++] = token_key(v, i);
+        }
+      }
+    __syncwarp();
+    if (total <= 6) {
+      for (int c = 0; c < total; ++c) list = token_insert(list, buffer[c], lane);
+    } else {
+      for (int c = 0; c < total; c += 32)
+        list = token_join(list, token_sort(c + lane < total ? buffer[c + lane] : 0ull, lane), lane);
+    }
+    __syncwarp();
+  } else {
+    // more than the buffer holds (many equal scores, or many alternatives): one by one
+#pragma unroll 1
+    for (int u = 0; u < U; ++u)
+#pragma unroll 1
+      for (int e = 0; e < V; ++e) {
+        const int i = first + u * stride + e;
+        const float v = u < n ? Elem<T>::to_f(z[i]) : __int_as_float(0x7FC00000);
+        list = token_offer(list, v >= bar_v ? token_key(v, i) : 0ull, top, lane);
+      }
+  }
+  const u64 last = __shfl_sync(0xffffffffu, list, top - 1);
+  if (last > bar) {
+    bar = last;
+    if (lane == 0) atomicMax(shared_bar, last);
+  }
+  return list;
+}
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kTokenThreads)
@@ -196,13 +284,17 @@ __global__ void __launch_bounds__(kTokenThreads)
     }
     return;
   }
+  if (TOP) {
+    if (tid == 0) sh.bar = 0;
+    __syncthreads();
+  }
 
   int head, nvec;
   row_split(z, P.cols, head, nvec);
   const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * rank / cluster);
   const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (rank + 1) / cluster);
   TokenSum s = {-INFINITY, 0.0f, 0.0f};
-  TokenBest best = {-INFINITY, 0x7FFFFFFF, -INFINITY, 0x7FFFFFFF};
+  u64 list = 0, bar = 0;
 
   for (int b = v0; b < v1; b += kTokenThreads * U) {
     uint4 r[U];
@@ -227,22 +319,20 @@ __global__ void __launch_bounds__(kTokenThreads)
       for (int e = 2; e < V; e += 2) mx = max3(mx, f[u * V + e], f[u * V + e + 1]);
       vmax[u] = mx;
     }
-    if constexpr (TOP) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = b + u * kTokenThreads + tid;
-        const bool ok = v < v1;
-        if (__any_sync(0xffffffffu, ok && vmax[u] >= best.thr_v)) {
-#pragma unroll 1
-          for (int e = 0; e < V; ++e)
-            token_offer(best, ok ? token_element<T>(r[u], e) : 0.0f, head + v * V + e, ok, P.top,
-                        lane);
-        }
-      }
-    }
     float bm = vmax[0];
 #pragma unroll
     for (int u = 1; u < U; ++u) bm = fmaxf(bm, vmax[u]);
+    if constexpr (TOP) {
+      bar = max_u64(bar, *static_cast<volatile u64*>(&sh.bar));
+      // (a lane's read of the shared bar may be older than another's: the warp takes lane 0's)
+      bar = __shfl_sync(0xffffffffu, bar, 0);
+      if (bar == 0 || __any_sync(0xffffffffu, bm >= token_key_value(bar))) {
+        const int v = b + tid;
+        const int n = v < v1 ? min(U, (v1 - v + kTokenThreads - 1) / kTokenThreads) : 0;
+        list = token_gather<T, U>(list, bar, f, vmax, bm, n, head + v * V, kTokenThreads * V, P.top,
+                                  z, sh.buffer[warp], &sh.bar, lane);
+      }
+    }
     token_add<U * V>(s, f, bm, k2);
   }
   if (warp == 0) {  // the unaligned ends: at most 7 scores each
@@ -254,8 +344,8 @@ __global__ void __launch_bounds__(kTokenThreads)
     const float f[2] = {zh, zt};
     token_add<2>(s, f, fmaxf(zh, zt), k2);
     if constexpr (TOP) {
-      token_offer(best, zh, lane, hd, P.top, lane);
-      token_offer(best, zt, tail + lane, tl, P.top, lane);
+      list = token_offer(list, hd && zh == zh ? token_key(zh, lane) : 0ull, P.top, lane);
+      list = token_offer(list, tl && zt == zt ? token_key(zt, tail + lane) : 0ull, P.top, lane);
     }
   }
 
@@ -269,37 +359,57 @@ __global__ void __launch_bounds__(kTokenThreads)
     s = (lane & o) ? token_merge(q, s, k2) : token_merge(s, q, k2);
   }
   if (lane == 0) sh.sum[warp] = s;
-  if (TOP) {
-    sh.best_v[warp][lane] = best.v;
-    sh.best_i[warp][lane] = best.i;
-  }
+  if (TOP) sh.best[warp][lane] = list;
   __syncthreads();
-  if (warp == 0) {
-    s = sh.sum[0];
-    for (int w = 1; w < kTokenWarps; ++w) s = token_merge(s, sh.sum[w], k2);
-    if constexpr (TOP) {
-      for (int w = 1; w < kTokenWarps; ++w) {
-        token_offer(best, sh.best_v[w][lane], sh.best_i[w][lane],
-                    lane < P.top && sh.best_i[w][lane] != 0x7FFFFFFF, P.top, lane);
+  if constexpr (TOP) {
+    // pairs of warps join their lists, then pairs of pairs
+#pragma unroll
+    for (int half = kTokenWarps / 2; half > 0; half >>= 1) {
+      if (warp < half) {
+        const u64 other = sh.best[warp + half][lane];
+        // (lists mostly end below the bar of another warp)
+        if (__any_sync(0xffffffffu, other > __shfl_sync(0xffffffffu, list, P.top - 1))) {
+          list = token_join(list, other, lane);
+          sh.best[warp][lane] = list;
+        }
       }
+      __syncthreads();
+    }
+  }
+  if (warp == 0) {
+    s = sh.sum[lane % kTokenWarps];  // (every eight lanes arrive at the same sum)
+#pragma unroll
+    for (int o = kTokenWarps / 2; o > 0; o >>= 1) {
+      TokenSum q;
+      q.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+      q.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+      q.a = __shfl_xor_sync(0xffffffffu, s.a, o);
+      s = (lane & o) ? token_merge(q, s, k2) : token_merge(s, q, k2);
     }
   }
   if (cluster > 1) {
     cg::cluster_group cl = cg::this_cluster();
     if (warp == 0) {
       if (lane == 0) sh.total = s;
-      sh.total_v[lane] = best.v;
-      sh.total_i[lane] = best.i;
+      sh.total_best[lane] = list;
     }
     cl.sync();
     if (rank == 0 && warp == 0) {
-      for (int q = 1; q < cluster; ++q) {
-        const TokenShared* o = cl.map_shared_rank(&sh, q);
-        s = token_merge(s, o->total, k2);
-        if constexpr (TOP)
-          token_offer(best, o->total_v[lane], o->total_i[lane],
-                      lane < P.top && o->total_i[lane] != 0x7FFFFFFF, P.top, lane);
-      }
+      TokenSum t[kTokenMaxCluster];
+      u64 o[kTokenMaxCluster];
+#pragma unroll
+      for (int q = 1; q < kTokenMaxCluster; ++q)
+        if (q < cluster) {
+          const TokenShared* other = cl.map_shared_rank(&sh, q);
+          t[q] = other->total;
+          if (TOP) o[q] = other->total_best[lane];
+        }
+#pragma unroll
+      for (int q = 1; q < kTokenMaxCluster; ++q)
+        if (q < cluster) {
+          s = token_merge(s, t[q], k2);
+          if (TOP) list = token_join(list, o[q], lane);
+        }
     }
     cl.sync();  // no CTA ends while its shared memory is read
     if (rank != 0) return;
@@ -315,11 +425,11 @@ __global__ void __launch_bounds__(kTokenThreads)
     if (P.stats) P.stats[row] = make_float2(s.m, empty ? 0.0f : log_l);
   }
   if (TOP && lane < P.top) {
-    const bool have = best.i != 0x7FFFFFFF;
+    const bool have = list != 0;
     P.top_logp[row * P.top + lane] =
-        empty ? -INFINITY : (have ? (best.v - s.m) * P.inv_eps - log_l
+        empty ? -INFINITY : (have ? (token_key_value(list) - s.m) * P.inv_eps - log_l
                                   : __int_as_float(0x7FC00000));
-    P.top_ids[row * P.top + lane] = have ? best.i : -1;
+    P.top_ids[row * P.top + lane] = have ? token_key_index(list) : -1;
   }
 }
 
