@@ -50,6 +50,30 @@ class PerDeviceOnce {
   std::atomic<uint64_t> done_{0};
 };
 
+// CTAs of a kernel that an SM holds at once, asked once per kernel and device.
+class PerDeviceOccupancy {
+ public:
+  int get(const void* fn, int threads, size_t smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 64;
+    if (dev < 64) {
+      const int n = known_[dev].load(std::memory_order_relaxed);
+      if (n > 0) return n;
+    }
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) {
+      cudaGetLastError();
+      n = 1;
+    }
+    if (n < 1) n = 1;
+    if (dev < 64) known_[dev].store(n, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  std::atomic<int> known_[64] = {};
+};
+
 // Launches `kernel` (a cluster of `cluster` CTAs along x when cluster > 1; kCooperative: all
 // CTAs resident at once, or an error).
 constexpr int kCooperative = -1;

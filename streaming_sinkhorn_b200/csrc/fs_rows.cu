@@ -47,9 +47,27 @@ int token_cluster(int64_t rows, int64_t cols, int vec) {
   const int64_t sms = current_sms();
   int c = 1;
   while (c < kTokenMaxCluster && rows * c < 2 * sms &&
-         cols >= 2ll * c * kTokenThreads * vec)
+         cols >= 2ll * c * TokenShape<8>::kRound / kTokenUnroll * vec)
     c *= 2;
   return c;
+}
+
+template <typename T, bool TOP, int NW>
+fs_status launch_tokens(const TokenParams& P, int cluster, cudaStream_t st) {
+  constexpr auto fn = token_logprobs_kernel<T, TOP, NW>;
+  static PerDeviceOnce once;
+  const fs_status s = once.run("cudaFuncSetAttribute", [&] {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TokenShape<NW>::kRing);
+  });
+  if (s != FS_OK) return s;
+  static PerDeviceOccupancy occupancy;
+  const int per_sm = occupancy.get(reinterpret_cast<const void*>(fn), NW * 32 + 32,
+                                   TokenShape<NW>::kRing);
+  const int64_t ctas =
+      cluster > 1 ? P.rows * cluster : std::min<int64_t>(P.rows, int64_t(per_sm) * current_sms());
+  return launch("fs_token_logprobs", fn, dim3(static_cast<unsigned>(ctas)), NW * 32 + 32,
+                TokenShape<NW>::kRing, st, cluster, P, cluster);
 }
 
 fs_status token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t ids_64,
@@ -83,9 +101,11 @@ fs_status token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
     const int c = token_cluster(z->rows, z->cols, Elem<T>::kVec);
-    const dim3 grid(static_cast<unsigned>(z->rows * c));
-    auto fn = top > 0 ? token_logprobs_kernel<T, true> : token_logprobs_kernel<T, false>;
-    return launch("fs_token_logprobs", fn, grid, kTokenThreads, 0, st, c, P, c);
+    // few rows: eight warps on each, for the shortest way through one; many: four, which pay a
+    // row's fixed costs half as often
+    if (P.rows * c < 4ll * current_sms())
+      return top > 0 ? launch_tokens<T, true, 8>(P, c, st) : launch_tokens<T, false, 8>(P, c, st);
+    return top > 0 ? launch_tokens<T, true, 4>(P, c, st) : launch_tokens<T, false, 4>(P, c, st);
   });
 }
 
@@ -127,12 +147,12 @@ fs_status token_logprobs_grad(const fs_matrix* z, float eps, const void* ids, in
   P.ld_grad = ld_grad;
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
-    const int64_t per = static_cast<int64_t>(kTokenThreads) * kTokenUnroll * Elem<T>::kVec;
+    const int64_t per = static_cast<int64_t>(kTokenGradThreads) * kTokenUnroll * Elem<T>::kVec;
     const int64_t chunks = (z->cols + per - 1) / per;
     if (chunks * z->rows > kMaxInt) return FS_ERR_SHAPE;
     P.chunks = static_cast<int32_t>(chunks);
     return launch("fs_token_logprobs_grad", token_logprobs_grad_kernel<T>,
-                  dim3(static_cast<unsigned>(chunks * z->rows)), kTokenThreads, 0, st, 1, P);
+                  dim3(static_cast<unsigned>(chunks * z->rows)), kTokenGradThreads, 0, st, 1, P);
   });
 }
 

@@ -9,10 +9,10 @@
 // overflow. The pass is bound by the read of the matrix: 1 exponential and about 6 other
 // instructions per score stay below it (4096 x 65536 bf16, forward: see kTokenThreads).
 //
-// Order of alternatives: larger z first, equal z by the lower index. Each warp keeps its best
-// (value, index) pairs as sorted whole numbers across its lanes, and the CTA the largest of the
-// warps' last kept pairs: a round of vectors is looked at one by one only where its maximum
-// reaches that bar, which after the first round happens about top * ln(n / n0) times a row.
+// Order of alternatives: larger z first, equal z by the lower index. The first round of a row
+// gives a bar that at least `top` scores reach; a warp sets the few vectors that reach it aside
+// and looks at their scores later, keeping its best (value, index) pairs as whole numbers sorted
+// across its lanes; the warps' lists are joined at the row's end.
 //
 // A row is read by one CTA, or by a cluster of up to 8 when there are few rows (a decoding
 // step), whose partial results meet in the first CTA through distributed shared memory: one
@@ -21,13 +21,14 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "fs_rowload.cuh"
+#include "fs_tcgen05.cuh"
 
 namespace fs {
 
-constexpr int kTokenThreads = 256;
-constexpr int kTokenWarps = kTokenThreads / 32;
-constexpr int kTokenUnroll = 4;  // 16-byte vectors in flight per thread
+constexpr int kTokenUnroll = 4;  // 16-byte vectors of a thread in one round
 constexpr int kTokenMaxTop = 32;
 constexpr int kTokenMaxCluster = 8;
 
@@ -65,9 +66,8 @@ __device__ __forceinline__ TokenSum token_merge(TokenSum x, TokenSum y, float k2
   return {m, x.l * sx + y.l * sy, sx * (x.a + x.l * cx) + sy * (y.a + y.l * cy)};
 }
 
-// Adds N scores to the running sums.
-template <int N>
-__device__ __forceinline__ void token_add(TokenSum& s, const float* z, float zmax, float k2) {
+// Moves the running sums to a new maximum.
+__device__ __forceinline__ void token_raise(TokenSum& s, float zmax, float k2) {
   if (zmax > s.m) {
     const float d = (s.m - zmax) * k2;
     const float sc = ex2(d);
@@ -75,34 +75,48 @@ __device__ __forceinline__ void token_add(TokenSum& s, const float* z, float zma
     s.l *= sc;
     s.m = zmax;
   }
+}
+
+// Adds N (even) scores to the running sums. A masked score has d = -inf and e = 0, and 0 * inf
+// must stay out of the entropy sum: d is clamped at -200, where e is 0 already.
+template <int N>
+__device__ __forceinline__ void token_add(TokenSum& s, const float* z, float zmax, float k2) {
+  token_raise(s, zmax, k2);
   const float mm = s.m == -INFINITY ? 0.0f : s.m;
-  if constexpr (N % 2 == 0) {
-    const u64 m2 = pk(mm, mm), kk = pk(k2, k2);
-    u64 l2 = pk(0.0f, 0.0f), a2 = pk(0.0f, 0.0f);
+  const u64 m2 = pk(-mm, -mm), kk = pk(k2, k2);
+  u64 l2 = pk(0.0f, 0.0f), a2 = pk(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const u64 d = mul2(sub2(pk(z[i], z[i + 1]), m2), kk);
-      float d0, d1;
-      upk(d, d0, d1);
-      const u64 e = pk(ex2(d0), ex2(d1));
-      l2 = add2(l2, e);
-      // a masked score has d = -inf and e = 0; below -200 e is 0 already
-      a2 = fma2(e, pk(fmaxf(d0, -200.0f), fmaxf(d1, -200.0f)), a2);
-    }
-    float x, y;
-    upk(l2, x, y);
-    s.l += x + y;
-    upk(a2, x, y);
-    s.a += x + y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = (z[i] - mm) * k2;
-      const float e = ex2(d);
-      s.l += e;
-      s.a += e * fmaxf(d, -200.0f);
-    }
+  for (int i = 0; i < N; i += 2) {
+    const u64 d = mul2(add2(pk(z[i], z[i + 1]), m2), kk);
+    float d0, d1;
+    upk(d, d0, d1);
+    const u64 e = pk(ex2(d0), ex2(d1));
+    l2 = add2(l2, e);
+    a2 = fma2(e, pk(fmaxf(d0, -200.0f), fmaxf(d1, -200.0f)), a2);
   }
+  float x, y;
+  upk(l2, x, y);
+  s.l += x + y;
+  upk(a2, x, y);
+  s.a += x + y;
+}
+
+// The sum of the parts of LANES neighbouring lanes, in every one of them: each part is brought
+// to the common maximum once, then both sums are added up.
+template <int LANES>
+__device__ __forceinline__ TokenSum token_reduce(TokenSum s, float k2) {
+  float m = s.m;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float d = (s.m - (m == -INFINITY ? 0.0f : m)) * k2;
+  const float sc = ex2(d);
+  float l = s.l * sc, a = sc * (s.a + s.l * fmaxf(d, -1.0e30f));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+  }
+  return {m, l, a};
 }
 
 // A score and its column as one whole number: larger score first, then the lower column. 0 is
@@ -121,9 +135,10 @@ __device__ __forceinline__ u64 min_u64(u64 a, u64 b) { return a < b ? a : b; }
 
 // The warp's keys, one per lane, sorted: the largest in lane 0 (bitonic, 15 exchanges).
 __device__ __forceinline__ u64 token_sort(u64 k, int lane) {
-#pragma unroll
+  // (rolled up, as is the join: the pass's loop should stay in the instruction cache)
+#pragma unroll 1
   for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
+#pragma unroll 1
     for (int o = size >> 1; o > 0; o >>= 1) {
       const u64 p = __shfl_xor_sync(0xffffffffu, k, o);
       k = ((lane & o) == 0) == ((lane & size) == 0) ? max_u64(k, p) : min_u64(k, p);
@@ -135,7 +150,7 @@ __device__ __forceinline__ u64 token_sort(u64 k, int lane) {
 // i-th last, which leaves a bitonic sequence, and five exchanges sort it.
 __device__ __forceinline__ u64 token_join(u64 a, u64 b, int lane) {
   a = max_u64(a, __shfl_sync(0xffffffffu, b, 31 - lane));
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     const u64 p = __shfl_xor_sync(0xffffffffu, a, o);
     a = (lane & o) == 0 ? max_u64(a, p) : min_u64(a, p);
@@ -161,279 +176,348 @@ __device__ __forceinline__ u64 token_offer(u64 list, u64 key, int top, int lane)
   return list;
 }
 
-// Candidates that a warp gathers from one round of vectors before it sorts them.
-constexpr int kTokenBuffer = 128;
+// Vectors that reach the bar, kept by a warp until it looks at their scores.
+constexpr int kTokenKept = 64;
 
-struct TokenShared {
-  TokenSum sum[kTokenWarps];
-  u64 best[kTokenWarps][32];
-  u64 buffer[kTokenWarps][kTokenBuffer];
-  // the largest of the warps' last kept keys: nothing below it is among the row's best
-  u64 bar;
-  // the CTA's result, read by the cluster's first CTA
-  TokenSum total;
-  u64 total_best[32];
+template <int NW>
+struct TokenShape {
+  static constexpr int kThreads = NW * 32;  // computing threads; one more warp copies
+  static constexpr int kRound = kThreads * kTokenUnroll;  // vectors of a stage
+  static constexpr uint32_t kStageBytes = kRound * 16u;
+  static constexpr int kStages = NW == 8 ? 3 : 4;
+  static constexpr int kRing = kStages * static_cast<int>(kStageBytes);
 };
 
-// Adds one round's vectors (f: U x V scores of this lane, the first of vector u at column
-// first + u * stride, n of them valid) to the warp's list. Gathers the scores above the bar in
-// shared memory, then inserts a few one by one or sorts and joins many at once. In the first
-// round the bar is raised beforehand: `top` lanes' maxima are at or above the top-th largest
-// of them, so whatever lies below that one is not among the row's best.
-template <typename T, int U>
-__device__ __forceinline__ u64 token_gather(u64 list, u64& bar, const float* f, const float* vmax,
-                                            float bm, int n, int first, int stride, int top,
-                                            const T* z, u64* buffer, u64* shared_bar, int lane) {
+template <int NW>
+struct TokenShared {
+  uint64_t full[TokenShape<NW>::kStages], empty[TokenShape<NW>::kStages];
+  int abort;  // a wait has expired: the rest of the CTA's rows are NaN
+  TokenSum sum[2][NW];  // by row parity: warps run ahead of the one that reads
+  TokenSum total;       // the CTA's result, read by the cluster's first CTA
+};
+template <int NW>
+struct TokenTop {  // alternatives
+  uint4 kept[NW][kTokenKept];
+  int kept_at[NW][kTokenKept];  // a vector's first column
+  u64 best[NW][32];
+  uint32_t maxima[NW][32];
+  u64 total_best[32];
+};
+struct TokenNoTop {};
+
+// Meeting point of the computing warps (the copying warp goes its own way).
+template <int NW>
+__device__ __forceinline__ void token_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+}
+
+// The bar of a row after its first round: the top-th largest of all threads' maxima (bm; have:
+// this thread has read a vector). At least `top` scores lie at or above it, and in a row of n
+// scores in random order about top * n / (scores of the round) do. Called by all computing
+// warps; each sorts its lanes' maxima out by `top` reductions, then merges the warps' lists.
+template <int NW>
+__device__ __forceinline__ float token_bar(float bm, bool have, int top, TokenTop<NW>& sh,
+                                           int warp, int lane) {
+  uint32_t mine = have && bm == bm ? order_key(bm) : 0u;
+  uint32_t sorted = 0u;
+  for (int r = 0; r < top; ++r) {
+    const uint32_t t = __reduce_max_sync(0xffffffffu, mine);
+    if (t == 0u) break;
+    if (lane == r) sorted = t;
+    // (equal maxima count one by one)
+    if (lane == __ffs(__ballot_sync(0xffffffffu, mine == t)) - 1) mine = 0u;
+  }
+  sh.maxima[warp][lane] = sorted;
+  token_sync<NW>();
+  int next = 0;
+  uint32_t head = lane < NW ? sh.maxima[lane][0] : 0u, t = 0u;
+  for (int r = 0; r < top; ++r) {
+    t = __reduce_max_sync(0xffffffffu, head);
+    if (t == 0u) break;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, head == t)) - 1) {
+      ++next;
+      head = next < 32 ? sh.maxima[lane][next] : 0u;
+    }
+  }
+  // with fewer than `top` maxima everything counts, -inf included
+  return t != 0u ? order_unkey(t) : -INFINITY;
+}
+
+// Looks at the scores of the warp's `n` kept vectors: those not below the bar go into the
+// sorted list, a few one by one, many sorted and joined. Raises the bar to the list's last
+// kept score.
+template <typename T>
+__device__ __noinline__ u64 token_look(u64 list, float& bar, const uint4* kept, const int* kept_at,
+                                       int n, int top, int lane) {
   constexpr int V = Elem<T>::kVec;
-  float bar_v = token_key_value(bar);
-  int bar_i = token_key_index(bar);
-  if (bar == 0) {
-    bar_v = -INFINITY;
-    bar_i = 0x7FFFFFFF;
-    uint32_t mine = n > 0 && bm == bm ? order_key(bm) : 0u, t = 0u;
-    for (int r = 0; r < top; ++r) {
-      t = __reduce_max_sync(0xffffffffu, mine);
-      if (t == 0u) break;
-      // (equal maxima count one by one)
-      const unsigned at = __ballot_sync(0xffffffffu, mine == t);
-      if (lane == __ffs(at) - 1) mine = 0u;
-    }
-    if (t != 0u) bar_v = order_unkey(t);
-  }
-  int count = 0;
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (u < n && vmax[u] >= bar_v) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float v = f[u * V + e];
-        count += v > bar_v || (v == bar_v && first + u * stride + e < bar_i);
-      }
-    }
-  int before = count;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int q = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += q;
-  }
-  const int total = __shfl_sync(0xffffffffu, before, 31);
-  if (total == 0) return list;
-  if (total <= kTokenBuffer) {
-    int at = before - count;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < n && vmax[u] >= bar_v) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float v = f[u * V + e];
-          const int i = first + u * stride + e;
-          if (v > bar_v || (v == bar_v && i < bar_i)) buffer[at++] = token_key(v, i);
-        }
-      }
-    __syncwarp();
-    if (total <= 6) {
-      for (int c = 0; c < total; ++c) list = token_insert(list, buffer[c], lane);
-    } else {
-      for (int c = 0; c < total; c += 32)
-        list = token_join(list, token_sort(c + lane < total ? buffer[c + lane] : 0ull, lane), lane);
-    }
-    __syncwarp();
-  } else {
-    // more than the buffer holds (many equal scores, or many alternatives): one by one
+  __syncwarp();
+  for (int c = 0; c < n; c += 32) {
+    const bool have = c + lane < n;
+    const T* x = reinterpret_cast<const T*>(kept + (have ? c + lane : 0));
+    const int at = have ? kept_at[c + lane] : 0;
 #pragma unroll 1
-    for (int u = 0; u < U; ++u)
-#pragma unroll 1
-      for (int e = 0; e < V; ++e) {
-        const int i = first + u * stride + e;
-        const float v = u < n ? Elem<T>::to_f(z[i]) : __int_as_float(0x7FC00000);
-        list = token_offer(list, v >= bar_v ? token_key(v, i) : 0ull, top, lane);
-      }
+    for (int e = 0; e < V; ++e) {
+      const float v = Elem<T>::to_f(x[e]);
+      const u64 key = have && v >= bar ? token_key(v, at + e) : 0ull;
+      const u64 last = __shfl_sync(0xffffffffu, list, top - 1);
+      const unsigned above = __ballot_sync(0xffffffffu, key > last);
+      if (__popc(above) > 6)
+        list = token_join(list, token_sort(key, lane), lane);
+      else if (above)
+        list = token_offer(list, key, top, lane);
+    }
   }
+  __syncwarp();
   const u64 last = __shfl_sync(0xffffffffu, list, top - 1);
-  if (last > bar) {
-    bar = last;
-    if (lane == 0) atomicMax(shared_bar, last);
-  }
+  if (last) bar = fmaxf(bar, token_key_value(last));
   return list;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kTokenThreads)
+// The part of a row that a CTA reads: `nvec` vectors from element `head` on are shared by the
+// cluster in order, vectors [v0, v1) are this CTA's.
+struct TokenPart {
+  int head, nvec, v0, v1;
+};
+template <typename T>
+__device__ __forceinline__ TokenPart token_part(const T* z, int cols, int rank, int cluster) {
+  TokenPart p;
+  row_split(z, cols, p.head, p.nvec);
+  p.v0 = static_cast<int>(static_cast<int64_t>(p.nvec) * rank / cluster);
+  p.v1 = static_cast<int>(static_cast<int64_t>(p.nvec) * (rank + 1) / cluster);
+  return p;
+}
+
+// CTAs stay and take rows blockIdx.x, + gridDim.x, ... (a cluster takes one row). The last warp
+// copies the CTA's parts of its rows, one after the other, into a ring in shared memory (bulk
+// copies), so the next row is on its way while the last one is summed up; NW warps compute.
+template <typename T, bool TOP, int NW>
+__global__ void __launch_bounds__(NW * 32 + 32, NW == 8 ? (TOP ? 3 : 4) : (TOP ? 5 : 6))
     token_logprobs_kernel(const TokenParams P, const int cluster) {
   namespace cg = cooperative_groups;
-  constexpr int V = Elem<T>::kVec, U = kTokenUnroll;
-  __shared__ TokenShared sh;
+  using H = TokenShape<NW>;
+  constexpr int V = Elem<T>::kVec, U = kTokenUnroll, S = H::kStages, NT = H::kThreads;
+  extern __shared__ __align__(128) unsigned char token_ring[];
+  __shared__ TokenShared<NW> sh;
+  __shared__ std::conditional_t<TOP, TokenTop<NW>, TokenNoTop> best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / cluster;
   const int rank = static_cast<int>(blockIdx.x % cluster);
-  const T* z = static_cast<const T*>(P.z) + row * P.ld;
+  const int64_t row0 = blockIdx.x / cluster, row_step = gridDim.x / cluster;
   const float k2 = P.inv_eps * kLog2e;
-  const int64_t id = ld_id(P.ids, row, P.ids_wide != 0);
-  if (id < 0) {  // nobody asks about this row (the same in all CTAs of its cluster)
-    if (rank == 0) {
-      if (tid == 0) {
-        P.logp[row] = 0.0f;
-        P.entropy[row] = 0.0f;
-        if (P.lse) P.lse[row] = 0.0f;
-        if (P.stats) P.stats[row] = make_float2(0.0f, 0.0f);
-      }
-      if (TOP && tid < P.top) {
-        P.top_logp[row * P.top + tid] = -INFINITY;
-        P.top_ids[row * P.top + tid] = -1;
+  volatile int* abort = &sh.abort;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], NW);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == NW) {
+    if (lane != 0) return;
+    int64_t q = 0;
+    bool ok = true;
+    for (int64_t row = row0; ok && row < P.rows; row += row_step) {
+      if (ld_id(P.ids, row, P.ids_wide != 0) < 0) continue;
+      const T* z = static_cast<const T*>(P.z) + row * P.ld;
+      const TokenPart p = token_part(z, P.cols, rank, cluster);
+      for (int b = p.v0; b < p.v1; b += H::kRound, ++q) {
+        const int i = static_cast<int>(q % S);
+        const uint32_t round = static_cast<uint32_t>(q / S);
+        if (round > 0 && !tc_wait(&sh.empty[i], (round - 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bytes = static_cast<uint32_t>(min(H::kRound, p.v1 - b)) * 16u;
+        mbar_expect_tx(&sh.full[i], bytes);
+        bulk_g2s(token_ring + i * H::kStageBytes, z + p.head + static_cast<int64_t>(b) * V, bytes,
+                 &sh.full[i]);
       }
     }
+    if (*abort)  // the copies in flight land before the CTA's shared memory goes
+      for (int64_t v = q > S ? q - S : 0; v < q; ++v)
+        (void)mbar_wait_bounded(&sh.full[v % S], static_cast<uint32_t>(v / S) & 1u);
     return;
   }
-  if (TOP) {
-    if (tid == 0) sh.bar = 0;
-    __syncthreads();
-  }
 
-  int head, nvec;
-  row_split(z, P.cols, head, nvec);
-  const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * rank / cluster);
-  const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (rank + 1) / cluster);
-  TokenSum s = {-INFINITY, 0.0f, 0.0f};
-  u64 list = 0, bar = 0;
-
-  for (int b = v0; b < v1; b += kTokenThreads * U) {
-    uint4 r[U];
-    float f[U * V];
-    float vmax[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = b + u * kTokenThreads + tid;
-      if (v < v1) r[u] = ld_stream(z + head + static_cast<int64_t>(v) * V);
+  // A wait that expires raises abort; every warp then goes on (each wait gives up soon), so that
+  // all still meet at the same barriers, and the rows come out as NaN.
+  int i = 0;           // stage
+  uint32_t phase = 0;  // of its barrier
+  int parity = 0;
+  // (each row's id and the given token's score are asked for before they are needed)
+  int64_t next_id = row0 < P.rows ? ld_id(P.ids, row0, P.ids_wide != 0) : 0;
+  for (int64_t row = row0; row < P.rows; row += row_step) {
+    const T* z = static_cast<const T*>(P.z) + row * P.ld;
+    const int64_t id = next_id;
+    if (row + row_step < P.rows) next_id = ld_id(P.ids, row + row_step, P.ids_wide != 0);
+    if (id < 0) {  // nobody asks about this row (the same in all CTAs of its cluster)
+      if (rank == 0) {
+        if (tid == 0) {
+          P.logp[row] = 0.0f;
+          P.entropy[row] = 0.0f;
+          if (P.lse) P.lse[row] = 0.0f;
+          if (P.stats) P.stats[row] = make_float2(0.0f, 0.0f);
+        }
+        if (TOP && tid < P.top) {
+          P.top_logp[row * P.top + tid] = -INFINITY;
+          P.top_ids[row * P.top + tid] = -1;
+        }
+      }
+      continue;
     }
+    const TokenPart p = token_part(z, P.cols, rank, cluster);
+    float zi = __int_as_float(0x7FC00000);
+    if (tid == 0 && rank == 0 && id < P.cols) zi = Elem<T>::to_f(z[id]);
+    TokenSum s = {-INFINITY, 0.0f, 0.0f};
+    u64 list = 0;
+    float bar = -INFINITY;
+    int kept = 0;
+    for (int b = p.v0; b < p.v1; b += H::kRound) {
+      (void)tc_wait(&sh.full[i], phase, abort);
+      const uint4* stage = reinterpret_cast<const uint4*>(token_ring + i * H::kStageBytes) + tid;
+      const int left = p.v1 - b - tid;  // vectors from this lane's first on
+      uint4 r[U];
+      if (p.v1 - b >= H::kRound) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = b + u * kTokenThreads + tid;
-      if (v < v1) {
-        Elem<T>::unpack(r[u], f + u * V);
+        for (int u = 0; u < U; ++u) r[u] = stage[u * NT];
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[u * V + e] = -INFINITY;
+        for (int u = 0; u < U; ++u) r[u] = u * NT < left ? stage[u * NT] : Elem<T>::masked();
       }
-      float mx = fmaxf(f[u * V], f[u * V + 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[i]);
+      if (++i == S) {
+        i = 0;
+        phase ^= 1u;
+      }
+      float f[U * V];
+      float vmax[U];
 #pragma unroll
-      for (int e = 2; e < V; e += 2) mx = max3(mx, f[u * V + e], f[u * V + e + 1]);
-      vmax[u] = mx;
-    }
-    float bm = vmax[0];
+      for (int u = 0; u < U; ++u) {
+        Elem<T>::unpack(r[u], f + u * V);
+        float mx = fmaxf(f[u * V], f[u * V + 1]);
 #pragma unroll
-    for (int u = 1; u < U; ++u) bm = fmaxf(bm, vmax[u]);
-    if constexpr (TOP) {
-      bar = max_u64(bar, *static_cast<volatile u64*>(&sh.bar));
-      // (a lane's read of the shared bar may be older than another's: the warp takes lane 0's)
-      bar = __shfl_sync(0xffffffffu, bar, 0);
-      if (bar == 0 || __any_sync(0xffffffffu, bm >= token_key_value(bar))) {
-        const int v = b + tid;
-        const int n = v < v1 ? min(U, (v1 - v + kTokenThreads - 1) / kTokenThreads) : 0;
-        list = token_gather<T, U>(list, bar, f, vmax, bm, n, head + v * V, kTokenThreads * V, P.top,
-                                  z, sh.buffer[warp], &sh.bar, lane);
+        for (int e = 2; e < V; e += 2) mx = max3(mx, f[u * V + e], f[u * V + e + 1]);
+        vmax[u] = mx;
+      }
+      float bm = vmax[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) bm = fmaxf(bm, vmax[u]);
+      token_add<U * V>(s, f, bm, k2);
+      if constexpr (TOP) {
+        if (b == p.v0) bar = token_bar<NW>(bm, left > 0, P.top, best, warp, lane);
+        if (__any_sync(0xffffffffu, bm >= bar)) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const bool reach = u * NT < left && vmax[u] >= bar;
+            const unsigned who = __ballot_sync(0xffffffffu, reach);
+            if (who) {
+              if (reach) {
+                const int at = kept + __popc(who & ((1u << lane) - 1u));
+                best.kept[warp][at] = r[u];
+                best.kept_at[warp][at] = p.head + (b + u * NT + tid) * V;
+              }
+              kept += __popc(who);
+              if (kept > kTokenKept - 32) {
+                list = token_look<T>(list, bar, best.kept[warp], best.kept_at[warp], kept, P.top,
+                                     lane);
+                kept = 0;
+              }
+            }
+          }
+        }
       }
     }
-    token_add<U * V>(s, f, bm, k2);
-  }
-  if (warp == 0) {  // the unaligned ends: at most 7 scores each
-    const int tail = head + nvec * V;
-    const bool hd = rank == 0 && lane < head;
-    const bool tl = rank == cluster - 1 && lane < P.cols - tail;
-    const float zh = hd ? Elem<T>::to_f(z[lane]) : -INFINITY;
-    const float zt = tl ? Elem<T>::to_f(z[tail + lane]) : -INFINITY;
-    const float f[2] = {zh, zt};
-    token_add<2>(s, f, fmaxf(zh, zt), k2);
-    if constexpr (TOP) {
-      list = token_offer(list, hd && zh == zh ? token_key(zh, lane) : 0ull, P.top, lane);
-      list = token_offer(list, tl && zt == zt ? token_key(zt, tail + lane) : 0ull, P.top, lane);
+    if constexpr (TOP)
+      list = token_look<T>(list, bar, best.kept[warp], best.kept_at[warp], kept, P.top, lane);
+    if (warp == 0) {  // the unaligned ends: at most 7 scores each
+      const int tail = p.head + p.nvec * V;
+      const bool hd = rank == 0 && lane < p.head;
+      const bool tl = rank == cluster - 1 && lane < P.cols - tail;
+      const float zh = hd ? Elem<T>::to_f(z[lane]) : -INFINITY;
+      const float zt = tl ? Elem<T>::to_f(z[tail + lane]) : -INFINITY;
+      const float f[2] = {zh, zt};
+      token_add<2>(s, f, fmaxf(zh, zt), k2);
+      if constexpr (TOP) {
+        list = token_offer(list, hd && zh == zh ? token_key(zh, lane) : 0ull, P.top, lane);
+        list = token_offer(list, tl && zt == zt ? token_key(zt, tail + lane) : 0ull, P.top, lane);
+      }
     }
-  }
 
+    s = token_reduce<32>(s, k2);
+    parity ^= 1;
+    if (lane == 0) sh.sum[parity][warp] = s;
+    if constexpr (TOP) best.best[warp][lane] = list;
+    token_sync<NW>();
+    if constexpr (TOP) {
+      // pairs of warps join their lists, then pairs of pairs
+#pragma unroll 1
+      for (int half = NW / 2; half > 0; half >>= 1) {
+        if (warp < half) {
+          const u64 other = best.best[warp + half][lane];
+          // (lists may end below another's last kept key)
+          if (__any_sync(0xffffffffu, other > __shfl_sync(0xffffffffu, list, P.top - 1))) {
+            list = token_join(list, other, lane);
+            best.best[warp][lane] = list;
+          }
+        }
+        token_sync<NW>();
+      }
+    }
+    if (warp == 0) {
+      s = token_reduce<NW>(sh.sum[parity][lane % NW], k2);
+      if (*abort) s.l = __int_as_float(0x7FC00000);
+    }
+    if (cluster > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      if (warp == 0) {
+        if (lane == 0) sh.total = s;
+        if constexpr (TOP) best.total_best[lane] = list;
+      }
+      cl.sync();  // (the copying warps leave by themselves)
+      if (rank == 0 && warp == 0) {
+        // lane c takes CTA c's sum
+        const int c0 = lane % kTokenMaxCluster;
+        s = token_reduce<kTokenMaxCluster>(c0 < cluster ? cl.map_shared_rank(&sh, c0)->total
+                                                        : TokenSum{-INFINITY, 0.0f, 0.0f},
+                                           k2);
+        if constexpr (TOP) {
+          u64 o[kTokenMaxCluster];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    TokenSum q;
-    q.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    q.l = __shfl_xor_sync(0xffffffffu, s.l, o);
-    q.a = __shfl_xor_sync(0xffffffffu, s.a, o);
-    // the lower lane's part first, so both lanes add in one order
-    s = (lane & o) ? token_merge(q, s, k2) : token_merge(s, q, k2);
-  }
-  if (lane == 0) sh.sum[warp] = s;
-  if (TOP) sh.best[warp][lane] = list;
-  __syncthreads();
-  if constexpr (TOP) {
-    // pairs of warps join their lists, then pairs of pairs
+          for (int c = 1; c < kTokenMaxCluster; ++c)
+            o[c] = c < cluster ? cl.map_shared_rank(&best, c)->total_best[lane] : 0ull;
 #pragma unroll
-    for (int half = kTokenWarps / 2; half > 0; half >>= 1) {
-      if (warp < half) {
-        const u64 other = sh.best[warp + half][lane];
-        // (lists mostly end below the bar of another warp)
-        if (__any_sync(0xffffffffu, other > __shfl_sync(0xffffffffu, list, P.top - 1))) {
-          list = token_join(list, other, lane);
-          sh.best[warp][lane] = list;
+          for (int c = 1; c < kTokenMaxCluster; ++c)
+            if (c < cluster) list = token_join(list, o[c], lane);
         }
       }
-      __syncthreads();
+      cl.sync();  // no CTA ends while its shared memory is read
     }
-  }
-  if (warp == 0) {
-    s = sh.sum[lane % kTokenWarps];  // (every eight lanes arrive at the same sum)
-#pragma unroll
-    for (int o = kTokenWarps / 2; o > 0; o >>= 1) {
-      TokenSum q;
-      q.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-      q.l = __shfl_xor_sync(0xffffffffu, s.l, o);
-      q.a = __shfl_xor_sync(0xffffffffu, s.a, o);
-      s = (lane & o) ? token_merge(q, s, k2) : token_merge(s, q, k2);
+    if (warp == 0 && rank == 0) {
+      const bool empty = s.m == -INFINITY && s.l == 0.0f;  // every score is -inf
+      const float log_l = logf(s.l);
+      if (lane == 0) {
+        P.logp[row] = empty ? (id < P.cols ? -INFINITY : zi) : (zi - s.m) * P.inv_eps - log_l;
+        P.entropy[row] = empty ? 0.0f : log_l - s.a / s.l * kLn2;
+        if (P.lse) P.lse[row] = empty ? -INFINITY : s.m * P.inv_eps + log_l;
+        if (P.stats) P.stats[row] = make_float2(s.m, empty ? 0.0f : log_l);
+      }
+      if (TOP && lane < P.top) {
+        const bool have = list != 0;
+        P.top_logp[row * P.top + lane] =
+            empty ? -INFINITY : (have ? (token_key_value(list) - s.m) * P.inv_eps - log_l
+                                      : __int_as_float(0x7FC00000));
+        P.top_ids[row * P.top + lane] = have ? token_key_index(list) : -1;
+      }
     }
-  }
-  if (cluster > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    if (warp == 0) {
-      if (lane == 0) sh.total = s;
-      sh.total_best[lane] = list;
-    }
-    cl.sync();
-    if (rank == 0 && warp == 0) {
-      TokenSum t[kTokenMaxCluster];
-      u64 o[kTokenMaxCluster];
-#pragma unroll
-      for (int q = 1; q < kTokenMaxCluster; ++q)
-        if (q < cluster) {
-          const TokenShared* other = cl.map_shared_rank(&sh, q);
-          t[q] = other->total;
-          if (TOP) o[q] = other->total_best[lane];
-        }
-#pragma unroll
-      for (int q = 1; q < kTokenMaxCluster; ++q)
-        if (q < cluster) {
-          s = token_merge(s, t[q], k2);
-          if (TOP) list = token_join(list, o[q], lane);
-        }
-    }
-    cl.sync();  // no CTA ends while its shared memory is read
-    if (rank != 0) return;
-  }
-  if (warp != 0) return;
-  const bool empty = s.m == -INFINITY && s.l == 0.0f;  // every score is -inf
-  const float log_l = logf(s.l);
-  if (lane == 0) {
-    const float zi = id < P.cols ? Elem<T>::to_f(z[id]) : __int_as_float(0x7FC00000);
-    P.logp[row] = empty ? (id < P.cols ? -INFINITY : zi) : (zi - s.m) * P.inv_eps - log_l;
-    P.entropy[row] = empty ? 0.0f : log_l - s.a / s.l * kLn2;
-    if (P.lse) P.lse[row] = empty ? -INFINITY : s.m * P.inv_eps + log_l;
-    if (P.stats) P.stats[row] = make_float2(s.m, empty ? 0.0f : log_l);
-  }
-  if (TOP && lane < P.top) {
-    const bool have = list != 0;
-    P.top_logp[row * P.top + lane] =
-        empty ? -INFINITY : (have ? (token_key_value(list) - s.m) * P.inv_eps - log_l
-                                  : __int_as_float(0x7FC00000));
-    P.top_ids[row * P.top + lane] = have ? token_key_index(list) : -1;
   }
 }
 
 // ---- gradient -------------------------------------------------------------------------------
+
+constexpr int kTokenGradThreads = 256;
 
 struct TokenGradParams {
   const void* z;
@@ -470,14 +554,14 @@ __device__ __forceinline__ float token_dscore(const TokenRow& r, float z, float 
   return ex2(t) * (r.c - r.ge * (fmaxf(t, -1.0e30f) * kLn2 + H));
 }
 
-// One CTA writes kTokenThreads * kTokenUnroll vectors of a row: one read, one exponential and
+// One CTA writes kTokenGradThreads * kTokenUnroll vectors of a row: one read, one exponential and
 // one write per score. The given token and the alternatives are rewritten afterwards from the
 // scores, their terms added in fp32 before the one rounding to the output's type.
 template <typename T>
-__global__ void __launch_bounds__(kTokenThreads)
+__global__ void __launch_bounds__(kTokenGradThreads)
     token_logprobs_grad_kernel(const TokenGradParams P) {
   constexpr int V = Elem<T>::kVec, U = kTokenUnroll;
-  constexpr int64_t kChunk = static_cast<int64_t>(kTokenThreads) * U * V;
+  constexpr int64_t kChunk = static_cast<int64_t>(kTokenGradThreads) * U * V;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / P.chunks;
   const int chunk = static_cast<int>(blockIdx.x % P.chunks);
@@ -505,18 +589,18 @@ __global__ void __launch_bounds__(kTokenThreads)
   int head, nvec;
   row_split(out, P.cols, head, nvec);
   const bool same = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const int64_t b = static_cast<int64_t>(chunk) * (kTokenThreads * U);
+  const int64_t b = static_cast<int64_t>(chunk) * (kTokenGradThreads * U);
   uint4 q[U];
   if (same && !zero) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t v = b + u * kTokenThreads + tid;
+      const int64_t v = b + u * kTokenGradThreads + tid;
       if (v < nvec) q[u] = ld_stream(z + head + v * V);
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t v = b + u * kTokenThreads + tid;
+    const int64_t v = b + u * kTokenGradThreads + tid;
     if (v >= nvec) break;
     float f[V];
     if (zero) {
