@@ -40,24 +40,18 @@ class Routing(NamedTuple):
     load: Any
 
 
-class _on:
-    """The data's device as the current one during a library call, and its current stream."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        cuda = _torch().cuda
-        self.before = cuda.current_device()
-        if self.before != self.index:
-            cuda.set_device(self.index)
-        return _torch()._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            _torch().cuda.set_device(self.before)
+def _call(fn, device, *args):
+    """A library call on ``device``'s current stream (its last argument), with ``device`` the
+    current one meanwhile."""
+    torch = _torch()
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _raise(code)
 
 
 _dtype_codes = {}
@@ -123,6 +117,29 @@ def _grad_ptr(g, keep):
     return g.data_ptr()
 
 
+def _workspace(size, device, *args):
+    """Scratch space of size(*args) bytes; a plan goes by the current device's SM count."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device.index:
+        nbytes = size(*args)
+    else:
+        with torch.cuda.device(device.index):
+            nbytes = size(*args)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _once(backward):
+    """``backward`` of a function that can be differentiated once: under create_graph its results
+    carry torch's marker that a second pass through them is an error."""
+    torch = _torch()
+    marked = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return marked(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return run
+
+
 # ---- log probabilities of given tokens ---------------------------------------------------------
 
 def _token_forward(logits, ids, eps, top, stats):
@@ -135,11 +152,9 @@ def _token_forward(logits, ids, eps, top, stats):
     st = torch.empty((n, 2), dtype=f32, device=dev) if stats else None
     tl = torch.empty((n, top), dtype=f32, device=dev) if top else None
     ti = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
-    with _on(dev) as stream:
-        _raise(_lib.load().fs_token_logprobs(
-            ctypes.byref(_matrix(logits)), eps, ids.data_ptr(), int(ids.dtype == torch.int64), top,
-            logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(st), _ptr(tl), _ptr(ti),
-            stream))
+    _call(_lib.load().fs_token_logprobs, dev, ctypes.byref(_matrix(logits)), eps, ids.data_ptr(),
+          int(ids.dtype == torch.int64), top, logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+          _ptr(st), _ptr(tl), _ptr(ti))
     return logp, entropy, lse, tl, ti, st
 
 
@@ -155,7 +170,6 @@ class _Functions:
     def get_token(cls):
         if cls.token is None:
             torch = _torch()
-            from torch.autograd.function import once_differentiable
 
             class TokenLogprobsFunction(torch.autograd.Function):
                 @staticmethod
@@ -169,18 +183,17 @@ class _Functions:
                     return logp, entropy, lse, tl, ti
 
                 @staticmethod
-                @once_differentiable
+                @_once
                 def backward(ctx, g_logp, g_entropy, g_lse, g_top, _):
                     logits, ids, entropy, st, ti = ctx.saved_tensors
                     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
                     keep = []
-                    with _on(logits.device) as stream:
-                        _raise(_lib.load().fs_token_logprobs_grad(
-                            ctypes.byref(_matrix(logits)), ctx.eps, ids.data_ptr(),
-                            int(ids.dtype == torch.int64), ctx.top, _ptr(ti), st.data_ptr(),
-                            entropy.data_ptr(), _grad_ptr(g_logp, keep), _grad_ptr(g_entropy, keep),
-                            _grad_ptr(g_lse, keep), _grad_ptr(g_top, keep), grad.data_ptr(),
-                            grad.shape[1], stream))
+                    _call(_lib.load().fs_token_logprobs_grad, logits.device,
+                          ctypes.byref(_matrix(logits)), ctx.eps, ids.data_ptr(),
+                          int(ids.dtype == torch.int64), ctx.top, _ptr(ti), st.data_ptr(),
+                          entropy.data_ptr(), _grad_ptr(g_logp, keep), _grad_ptr(g_entropy, keep),
+                          _grad_ptr(g_lse, keep), _grad_ptr(g_top, keep), grad.data_ptr(),
+                          grad.shape[1])
                     return grad, None, None, None
 
             cls.token = TokenLogprobsFunction
@@ -190,7 +203,6 @@ class _Functions:
     def get_linear(cls):
         if cls.linear is None:
             torch = _torch()
-            from torch.autograd.function import once_differentiable
 
             class LinearLogprobsFunction(torch.autograd.Function):
                 @staticmethod
@@ -202,7 +214,7 @@ class _Functions:
                     return logp, entropy, lse
 
                 @staticmethod
-                @once_differentiable
+                @_once
                 def backward(ctx, g_logp, g_entropy, g_lse):
                     x, w, ids, entropy, st = ctx.saved_tensors
                     gx, gw = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
@@ -210,14 +222,11 @@ class _Functions:
                     lib = _lib.load()
                     mx, mw = ctypes.byref(_matrix(x)), ctypes.byref(_matrix(w))
                     keep = []
-                    with _on(x.device) as stream:
-                        ws = torch.empty(lib.fs_linear_logprobs_grad_workspace_bytes(mx, mw),
-                                         dtype=torch.uint8, device=x.device)
-                        _raise(lib.fs_linear_logprobs_grad(
-                            mx, mw, ctx.eps, ids.data_ptr(), int(ids.dtype == torch.int64),
-                            st.data_ptr(), entropy.data_ptr(), _grad_ptr(g_logp, keep),
-                            _grad_ptr(g_entropy, keep), _grad_ptr(g_lse, keep), _ptr(gx), _ptr(gw),
-                            ws.data_ptr(), ws.numel(), stream))
+                    ws = _workspace(lib.fs_linear_logprobs_grad_workspace_bytes, x.device, mx, mw)
+                    _call(lib.fs_linear_logprobs_grad, x.device, mx, mw, ctx.eps, ids.data_ptr(),
+                          int(ids.dtype == torch.int64), st.data_ptr(), entropy.data_ptr(),
+                          _grad_ptr(g_logp, keep), _grad_ptr(g_entropy, keep),
+                          _grad_ptr(g_lse, keep), _ptr(gx), _ptr(gw), ws.data_ptr(), ws.numel())
                     return gx, gw, None, None
 
             cls.linear = LinearLogprobsFunction
@@ -227,7 +236,6 @@ class _Functions:
     def get_routing(cls):
         if cls.routing is None:
             torch = _torch()
-            from torch.autograd.function import once_differentiable
 
             class RouteFunction(torch.autograd.Function):
                 @staticmethod
@@ -242,19 +250,18 @@ class _Functions:
                     return weights, ids, counts
 
                 @staticmethod
-                @once_differentiable
+                @_once
                 def backward(ctx, g_weights, _ids, _load):
                     if g_weights is None:
                         return None, None, None, None
                     logits, weights, ids = ctx.saved_tensors
                     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
                     keep = []
-                    with _on(logits.device) as stream:
-                        _raise(_lib.load().fs_route_grad(
-                            ctypes.byref(_matrix(logits)),
-                            ctypes.byref(_lib.fs_route_options(*ctx.options, None)),
-                            weights.data_ptr(), ids.data_ptr(), _grad_ptr(g_weights, keep),
-                            grad.data_ptr(), stream))
+                    _call(_lib.load().fs_route_grad, logits.device,
+                          ctypes.byref(_matrix(logits)),
+                          ctypes.byref(_lib.fs_route_options(*ctx.options, None)),
+                          weights.data_ptr(), ids.data_ptr(), _grad_ptr(g_weights, keep),
+                          grad.data_ptr())
                     return grad, None, None, None
 
             cls.routing = RouteFunction
@@ -297,12 +304,9 @@ def _linear_forward(x, w, ids, eps, stats):
     st = torch.empty((n, 2), dtype=f32, device=dev) if stats else None
     lib = _lib.load()
     mx, mw = ctypes.byref(_matrix(x)), ctypes.byref(_matrix(w))
-    with _on(dev) as stream:
-        ws = torch.empty(lib.fs_linear_logprobs_workspace_bytes(mx, mw), dtype=torch.uint8,
-                         device=dev)
-        _raise(lib.fs_linear_logprobs(mx, mw, eps, ids.data_ptr(), int(ids.dtype == torch.int64),
-                                      logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
-                                      _ptr(st), ws.data_ptr(), ws.numel(), stream))
+    ws = _workspace(lib.fs_linear_logprobs_workspace_bytes, dev, mx, mw)
+    _call(lib.fs_linear_logprobs, dev, mx, mw, eps, ids.data_ptr(), int(ids.dtype == torch.int64),
+          logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(st), ws.data_ptr(), ws.numel())
     return logp, entropy, lse, st
 
 
@@ -352,10 +356,9 @@ def _route_forward(logits, bias, options, load):
     weights = torch.empty((n, k), dtype=torch.float32, device=dev)
     ids = torch.empty((n, k), dtype=torch.int32, device=dev)
     counts = torch.empty(e, dtype=torch.int32, device=dev) if load else None
-    with _on(dev) as stream:
-        _raise(_lib.load().fs_route(ctypes.byref(_matrix(logits)),
-                                    ctypes.byref(_lib.fs_route_options(*options, _ptr(bias))),
-                                    weights.data_ptr(), ids.data_ptr(), _ptr(counts), stream))
+    _call(_lib.load().fs_route, dev, ctypes.byref(_matrix(logits)),
+          ctypes.byref(_lib.fs_route_options(*options, _ptr(bias))), weights.data_ptr(),
+          ids.data_ptr(), _ptr(counts))
     return weights, ids, counts
 
 
@@ -422,11 +425,8 @@ def balance(logits, *, score: str = "softmax", eps: float, n_iters: int, load=No
     f = torch.empty(n, dtype=torch.float32, device=dev)
     g = torch.empty(e, dtype=torch.float32, device=dev)
     lib = _lib.load()
-    m = _matrix(logits)
-    with _on(dev) as stream:
-        nbytes = lib.fs_balance_workspace_bytes(ctypes.byref(m))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _raise(lib.fs_balance(ctypes.byref(m), _score_code(score), float(eps), int(n_iters),
-                              _ptr(load), _ptr(g_init), f.data_ptr(), g.data_ptr(), ws.data_ptr(),
-                              ws.numel(), stream))
+    m = ctypes.byref(_matrix(logits))
+    ws = _workspace(lib.fs_balance_workspace_bytes, dev, m)
+    _call(lib.fs_balance, dev, m, _score_code(score), float(eps), int(n_iters), _ptr(load),
+          _ptr(g_init), f.data_ptr(), g.data_ptr(), ws.data_ptr(), ws.numel())
     return f, g
