@@ -11,13 +11,15 @@
 // fast path works in fp32 with a bound on its error, and a row in which two neighbours of
 // the order (the last pick and the first that is left included) lie within their bounds is
 // done over in 64 bits by the same warp. Experts of equal logit and bias are equal in any
-// precision and need no second look. About one row in 500 is done over on normal logits of
+// precision and need no second look. About one row in 1000 is done over on normal logits of
 // 256 experts.
 //
-// One warp takes a row: lane l holds experts l, l + 32, ... as whole-number keys that order
-// like c, and each pick is two warp reductions (the largest key, the lowest index holding
-// it).
+// One warp takes a row, each lane a few neighbouring experts, as whole-number keys that order
+// like c. What bounds it is instructions: about 500 a row at 256 experts, 8 of them picked out
+// of 4 of 8 groups.
 #pragma once
+
+#include <cfloat>
 
 #include "fs_rowload.cuh"
 
@@ -27,6 +29,12 @@ constexpr int kRouteWarps = 8;
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 31;       // lane k holds the first expert left out
 constexpr int kRouteMaxGroups = 32;  // one bit each in a mask
+
+// Doubles of a warp's scratch: one per expert, at least 32 candidates of 16 bytes, and whole
+// 16-byte units, so that every warp's candidates are aligned.
+__host__ __device__ constexpr int route_room(int experts) {
+  return experts < 64 ? 64 : (experts + 1) / 2 * 2;
+}
 
 enum RouteScore : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 
@@ -65,13 +73,28 @@ __device__ __forceinline__ double route_score64(double z, int kind, double m, do
   return kind == kScoreSigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / sum;
 }
 
-// Bound on the error of c = s + b in fp32. exp's argument x carries 2^-24 |x| twice (the
-// difference or product, and its rounding), ex2 2^-22, the sum and the quotient a few 2^-24;
-// s inherits them as relative errors, c one more rounding, and a score below 2^-126 is
-// flushed. Doubled against what was left out.
-__device__ __forceinline__ float route_err(float z, float s, float c, int kind, float m) {
-  const float x = kind == kScoreSigmoid ? fabsf(z) : m - z;
-  return s * (x + 8.0f) * 0x1p-21f + fabsf(c) * 0x1p-23f + 0x1p-124f;
+// Bounds on the error of c = s + b in fp32, u = 2^-24.
+// Sigmoid: e = ex2(-z log2 e) is off by 2 |z| u (product, constant) + 4 u (ex2); s = 1 / (1 + e)
+// takes (1 - s) of that, u for the sum and 4 u for the quotient: s ((1 - s) (2 |z| + 4) u + 5 u).
+// Softmax, d = m - z: e is off by 3 d u + 4 u, the sum by the e-weighted mean of the same, at
+// most 3 ln(1024) u + 4 u, and 12 u of additions, inverse and product by 4 u:
+// s (3 d + 45) u. c rounds once more, |c| u; scores below 2^-126 are flushed. All times 1.5.
+__device__ __forceinline__ float route_err(float z, float s, float c, bool sig, float m) {
+  constexpr float u = 1.5f * 0x1p-24f;
+  const float e = sig ? s * ((1.0f - s) * (2.0f * fabsf(z) + 4.0f) + 5.0f) : s * (3.0f * (m - z) + 45.0f);
+  return e * u + fabsf(c) * u + 0x1p-124f;
+}
+// The same for the sum of a group's two best, whichever they are: s (1 - s) (2 |z| + 4) <= 1.5
+// for sigmoid; s <= inv, the largest score, and s d <= inv for softmax.
+__device__ __forceinline__ float route_group_err(float sum, bool sig, float inv) {
+  constexpr float u = 1.5f * 0x1p-24f;
+  return (2.0f * (sig ? 6.5f : 48.0f * inv) + 3.0f * fabsf(sum) + 4.0f) * u;
+}
+
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // A row whose maximum or sum shows NaN (a NaN logit or bias, +inf under softmax) has no
@@ -160,53 +183,159 @@ __device__ __noinline__ void route_row64(const RouteParams& P, const T* z, int64
   route_write(P, row, lane, mine, tot > 0.0 ? static_cast<float>(P.scale * (s / tot)) : 0.0f);
 }
 
-// NL: experts per lane. Dynamic shared memory: experts doubles per warp, then the CTA's load.
-template <typename T, int NL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams P) {
+// The k + 1 best c of the warp in order, the r-th in lane r (-inf stands for a closed expert;
+// lane l holds experts l * NL + i; c is used up). Pick by pick: the largest c by one warp
+// reduction, the lowest lane and in it the lowest index that holds it.
+template <int NL>
+__device__ __forceinline__ void route_pick_each(float* c, int k, int lane, int& mine,
+                                                float& mine_c) {
+  float lc = c[0];
+  int li = 0;
+#pragma unroll
+  for (int i = 1; i < NL; ++i)
+    if (c[i] > lc) {
+      lc = c[i];
+      li = i;
+    }
+  for (int r = 0; r <= k; ++r) {
+    const float top = redux_max(lc);
+    if (top == -INFINITY) break;
+    const int src = __ffs(__ballot_sync(0xffffffffu, lc == top)) - 1;
+    const int at = __shfl_sync(0xffffffffu, lane * NL + li, src);
+    if (lane == r) {
+      mine = at;
+      mine_c = top;
+    }
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (i == li) c[i] = -INFINITY;
+      lc = c[0];
+      li = 0;
+#pragma unroll
+      for (int i = 1; i < NL; ++i)
+        if (c[i] > lc) {
+          lc = c[i];
+          li = i;
+        }
+    }
+  }
+}
+
+// The same by way of candidates, for few picks of many experts: the (k + 1)-th largest value
+// among the lanes' maxima is a bar that at least k + 1 scores reach and about
+// -32 ln(1 - (k + 1) / 32) do (10 for k = 8). They are set aside, each lane takes one and counts
+// those ahead of it. False (nothing picked) where more than 32 reach the bar.
+template <int NL>
+__device__ __forceinline__ bool route_pick_few(const float* c, const float* z, int k, int lane,
+                                               float4* buffer, int& mine, float& mine_c,
+                                               float& mine_z) {
+  float lc = c[0];
+#pragma unroll
+  for (int i = 1; i < NL; ++i) lc = fmaxf(lc, c[i]);
+  float bar = -INFINITY;
+  for (int r = 0; r <= k; ++r) {
+    bar = redux_max(lc);  // (equal maxima count once: the bar only gets lower)
+    if (lc == bar) lc = -INFINITY;
+  }
+  // fewer lanes than that have an open expert: every open one counts
+  if (bar == -INFINITY) bar = -FLT_MAX;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) count += c[i] >= bar;
+  int before = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int q = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += q;
+  }
+  const int total = __shfl_sync(0xffffffffu, before, 31);
+  if (total > 32) return false;
+  if (count) {
+    int at = before - count;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (c[i] >= bar) buffer[at++] = make_float4(c[i], __int_as_float(lane * NL + i), z[i], 0.0f);
+  }
+  __syncwarp();
+  const float4 my = buffer[lane];
+  int ahead = 0;
+#pragma unroll 4
+  for (int t = 0; t < total; ++t) {
+    // (set aside by ascending expert: of equal scores the earlier ones are ahead)
+    const float o = buffer[t].x;
+    ahead += o > my.x || (o == my.x && t < lane);
+  }
+  __syncwarp();
+  if (lane < total) buffer[ahead] = my;
+  __syncwarp();
+  if (lane <= k && lane < total) {
+    const float4 o = buffer[lane];
+    mine = __float_as_int(o.y);
+    mine_c = o.x;
+    mine_z = o.z;
+  }
+  __syncwarp();
+  return true;
+}
+
+// Picks of at most this many go by way of candidates where a lane holds several experts.
+constexpr int kRouteFew = 12;
+
+// NL: experts per lane, lane l holding l * NL .. + NL - 1. Dynamic shared memory: route_room
+// doubles per warp, then the CTA's load.
+template <typename T, int NL, bool SIG>
+__global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kernel(const RouteParams P) {
   extern __shared__ __align__(16) unsigned char route_smem[];
+  constexpr int kind = SIG ? kScoreSigmoid : kScoreSoftmax;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = P.experts;
-  double* c64 = reinterpret_cast<double*>(route_smem) + warp * E;
+  const int room = route_room(E);
+  double* c64 = reinterpret_cast<double*>(route_smem) + warp * room;
   float* c32 = reinterpret_cast<float*>(c64);
   int* hist = nullptr;
   if (P.load) {
-    hist = reinterpret_cast<int*>(reinterpret_cast<double*>(route_smem) + kRouteWarps * E);
+    hist = reinterpret_cast<int*>(reinterpret_cast<double*>(route_smem) + kRouteWarps * room);
     for (int j = threadIdx.x; j < E; j += blockDim.x) hist[j] = 0;
     __syncthreads();
   }
-  const bool sig = P.score == kScoreSigmoid;
+  const int j0 = lane * NL;
+  // whole lanes of a power of two of them make up a group: its two best meet by shuffles
+  const int group_lanes = P.per_group / NL;
+  const bool by_lanes = P.per_group % NL == 0 && (group_lanes & (group_lanes - 1)) == 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; row < P.rows;
        row += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
     const T* z = static_cast<const T*>(P.z) + row * P.ld;
     float v[NL];
+    constexpr int V = Elem<T>::kVec;
+    if (NL % V == 0 && E == 32 * NL && (reinterpret_cast<uintptr_t>(z) & 15u) == 0) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int j = lane + 32 * i;
-      v[i] = j < E ? Elem<T>::to_f(z[j]) : -INFINITY;
+      for (int i = 0; i < NL / V; ++i)
+        Elem<T>::unpack(ld_stream(z + j0 + i * V), v + i * V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) v[i] = j0 + i < E ? Elem<T>::to_f(z[j0 + i]) : -INFINITY;
     }
     float m = 0.0f, inv = 1.0f;
-    if (!sig) {
+    if (!SIG) {
       m = v[0];
 #pragma unroll
       for (int i = 1; i < NL; ++i) m = fmaxf(m, v[i]);
-      m = warp_maxf(m);
+      m = redux_max(m);
       float sum = 0.0f;
       const float mm = m == -INFINITY ? 0.0f : m;
 #pragma unroll
       for (int i = 0; i < NL; ++i) sum += ex2((v[i] - mm) * kLog2e);
       inv = 1.0f / warp_sumf(sum);
     }
-    uint32_t key[NL];
+    float c[NL];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int j = lane + 32 * i;
-      float c = route_score(v[i], P.score, m, inv);
-      if (P.bias && j < E) c += P.bias[j];
-      // closed: a logit or a bias of -inf
-      const bool open = v[i] != -INFINITY && c != -INFINITY;
-      bad |= open && c != c;
-      key[i] = open ? order_key(c) : 0u;
+      c[i] = route_score(v[i], kind, m, inv);
+      if (P.bias && j0 + i < E) c[i] += P.bias[j0 + i];
+      if (v[i] == -INFINITY) c[i] = -INFINITY;  // closed
+      bad |= c[i] != c[i];
     }
     if (__any_sync(0xffffffffu, bad)) {
       route_write(P, row, lane, -1, __int_as_float(0x7FC00000));
@@ -214,98 +343,89 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     }
     bool again = false;  // a border too close for fp32
     if (P.groups > 1) {
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        if (lane + 32 * i < E) c32[lane + 32 * i] = key[i] ? order_unkey(key[i]) : -INFINITY;
-      __syncwarp();
-      // the two largest of each group: `lanes` neighbouring lanes scan one group
-      int lanes = 32;
-      while (lanes * P.groups > 32) lanes >>= 1;
-      const int g = lane / lanes;
       float a = -INFINITY, b = -INFINITY;
-      if (g < P.groups)
-        for (int j = lane % lanes; j < P.per_group; j += lanes) {
-          const float x = c32[g * P.per_group + j];
-          b = fmaxf(b, fminf(a, x));
-          a = fmaxf(a, x);
+      int g, lanes;  // this lane's group, and how many lanes share it
+      if (by_lanes) {
+        g = lane / group_lanes;
+        lanes = group_lanes;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          b = fmaxf(b, fminf(a, c[i]));
+          a = fmaxf(a, c[i]);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          if (j0 + i < E) c32[j0 + i] = c[i];
+        __syncwarp();
+        lanes = 32;
+        while (lanes * P.groups > 32) lanes >>= 1;
+        g = lane / lanes;
+        if (g < P.groups)
+          for (int j = lane % lanes; j < P.per_group; j += lanes) {
+            const float x = c32[g * P.per_group + j];
+            b = fmaxf(b, fminf(a, x));
+            a = fmaxf(a, x);
+          }
+      }
       for (int o = 1; o < lanes; o <<= 1) {
         const float oa = __shfl_xor_sync(0xffffffffu, a, o);
         const float ob = __shfl_xor_sync(0xffffffffu, b, o);
         b = fmaxf(fmaxf(b, ob), fminf(a, oa));
         a = fmaxf(a, oa);
       }
-      const float gs = g >= P.groups || a == -INFINITY ? -INFINITY : (b == -INFINITY ? a : a + b);
-      int ahead = 0;
-      for (int q = 0; q < P.groups; ++q) {
-        const float o = __shfl_sync(0xffffffffu, gs, q * lanes);
-        ahead += o > gs || (o == gs && q < g);
+      const float gs = g >= P.groups ? -INFINITY : (b == -INFINITY ? a : a + b);
+      // kept: the groups down to the top_groups-th largest sum; where equal sums make it more,
+      // or the next sum is near, 64 bits decide
+      float left = gs, lo = -INFINITY;
+      for (int r = 0; r < P.top_groups; ++r) {
+        const float t = redux_max(left);
+        if (t != -INFINITY) lo = t;
+        if (left == t) left = -INFINITY;
       }
-      const bool kept = g < P.groups && ahead < P.top_groups;
-      // the border between kept and dropped groups; each score is off by at most 20 * 2^-21
-      const float lo = -warp_maxf(kept ? -gs : -INFINITY);
-      const float hi = warp_maxf(g < P.groups && !kept ? gs : -INFINITY);
-      again = hi != -INFINITY &&
-              !(lo - hi > 80.0f * 0x1p-21f + (fabsf(lo) + fabsf(hi)) * 0x1p-22f);
-      if (g < P.groups && !kept)
-        for (int j = lane % lanes; j < P.per_group; j += lanes) c32[g * P.per_group + j] = -INFINITY;
-      __syncwarp();
+      const bool kept = gs >= lo && gs != -INFINITY;
+      const float hi = redux_max(left);
+      again = (hi != -INFINITY && !(lo - hi > route_group_err(lo, SIG, inv) +
+                                                 route_group_err(hi, SIG, inv))) ||
+              __popc(__ballot_sync(0xffffffffu, kept && lane % lanes == 0)) > P.top_groups;
+      if (by_lanes) {
+        if (!kept) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i)
-        if (lane + 32 * i < E && c32[lane + 32 * i] == -INFINITY) key[i] = 0u;
-      __syncwarp();
-    }
-    // k picks and the first expert left out
-    uint32_t lk = key[0];
-    int li = lane;
-#pragma unroll
-    for (int i = 1; i < NL; ++i)
-      if (key[i] > lk) {
-        lk = key[i];
-        li = lane + 32 * i;
-      }
-    int mine = -1;
-    uint32_t mine_key = 0u;
-    for (int r = 0; r <= P.k; ++r) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, lk);
-      if (top == 0u) break;
-      const int at = static_cast<int>(
-          __reduce_min_sync(0xffffffffu, lk == top ? static_cast<unsigned>(li) : 0x7FFFFFFFu));
-      if (lane == r) {
-        mine = at;
-        mine_key = top;
-      }
-      if ((at & 31) == lane) {
+          for (int i = 0; i < NL; ++i) c[i] = -INFINITY;
+        }
+      } else {
+        if (g < P.groups && !kept)
+          for (int j = lane % lanes; j < P.per_group; j += lanes)
+            c32[g * P.per_group + j] = -INFINITY;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NL; ++i)
-          if (lane + 32 * i == at) key[i] = 0u;
-        lk = key[0];
-        li = lane;
-#pragma unroll
-        for (int i = 1; i < NL; ++i)
-          if (key[i] > lk) {
-            lk = key[i];
-            li = lane + 32 * i;
-          }
+          if (j0 + i < E) c[i] = c32[j0 + i];
+        __syncwarp();
       }
     }
-    float zr = 0.0f, s = 0.0f, br = 0.0f, c = 0.0f, err = 0.0f;
-    if (mine >= 0) {
-      zr = Elem<T>::to_f(z[mine]);
-      s = route_score(zr, P.score, m, inv);
-      br = P.bias ? P.bias[mine] : 0.0f;
-      c = order_unkey(mine_key);
-      err = route_err(zr, s, c, P.score, m);
+    int mine = -1;
+    float cr = -INFINITY;
+    float zr = 0.0f, s = 0.0f, br = 0.0f, err = 0.0f;
+    if (!(NL > 1 && P.k <= kRouteFew &&
+          route_pick_few<NL>(c, v, P.k, lane, reinterpret_cast<float4*>(c64), mine, cr, zr))) {
+      route_pick_each<NL>(c, P.k, lane, mine, cr);
+      if (mine >= 0) zr = Elem<T>::to_f(z[mine]);
     }
-    const int nmine = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (mine >= 0) {
+      s = route_score(zr, kind, m, inv);
+      br = P.bias ? P.bias[mine] : 0.0f;
+      err = route_err(zr, s, cr, SIG, m);
+    }
     const float nz = __shfl_down_sync(0xffffffffu, zr, 1);
     const float nb = __shfl_down_sync(0xffffffffu, br, 1);
-    const float nc = __shfl_down_sync(0xffffffffu, c, 1);
+    const float nc = __shfl_down_sync(0xffffffffu, cr, 1);
     const float ne = __shfl_down_sync(0xffffffffu, err, 1);
-    again |= lane < P.k && mine >= 0 && nmine >= 0 && !(c - nc > err + ne) &&
-             !(zr == nz && br == nb);
-    // a score that fp32 flushes also loses its weight
-    again |= lane < P.k && mine >= 0 && s < 0x1p-100f;
+    if (lane < P.k && mine >= 0) {
+      again |= nc != -INFINITY && !(cr - nc > err + ne) && !(zr == nz && br == nb);
+      // a score that fp32 flushes also loses its weight
+      again |= s < 0x1p-100f;
+    }
     if (__any_sync(0xffffffffu, again)) {
       route_row64(P, z, row, c64, hist, lane);
       __syncwarp();
@@ -317,7 +437,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     }
     const float tot = P.renorm ? warp_sumf(s) : 1.0f;
     if (hist && mine >= 0) atomicAdd(&hist[mine], 1);
-    route_write(P, row, lane, mine, tot > 0.0f ? P.scale * (s / tot) : 0.0f);
+    route_write(P, row, lane, mine, tot > 0.0f ? P.scale * __fdividef(s, tot) : 0.0f);
   }
   if (P.load) {
     // whole numbers: the order of the atomics changes nothing

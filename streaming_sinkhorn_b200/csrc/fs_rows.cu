@@ -173,15 +173,38 @@ fs_status check_route(const fs_matrix* z, const fs_route_options* o) {
   return FS_OK;
 }
 
-// Experts per lane, rounded up to a power of two: 1 .. 32.
+// Experts per lane of a warp, rounded up to one of these.
 template <typename F>
 fs_status by_width(int64_t experts, F&& f) {
   if (experts <= 32) return f(std::integral_constant<int, 1>());
   if (experts <= 64) return f(std::integral_constant<int, 2>());
   if (experts <= 128) return f(std::integral_constant<int, 4>());
+  if (experts <= 160) return f(std::integral_constant<int, 5>());
   if (experts <= 256) return f(std::integral_constant<int, 8>());
+  if (experts <= 384) return f(std::integral_constant<int, 12>());
   if (experts <= 512) return f(std::integral_constant<int, 16>());
   return f(std::integral_constant<int, 32>());
+}
+
+template <typename T, int NL, bool SIG>
+fs_status launch_route(const RouteParams& P, int64_t ctas, size_t smem, cudaStream_t st) {
+  constexpr auto fn = route_kernel<T, NL, SIG>;
+  static PerDeviceOnce once;
+  const fs_status s = once.run("cudaFuncSetAttribute", [&] {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                FS_MAX_EXPERTS * (kRouteWarps * 8 + 4));
+  });
+  if (s != FS_OK) return s;
+  // with a load to count, CTAs stay and take several rows each, so that few histograms are
+  // added up
+  if (P.load) {
+    static PerDeviceOccupancy occupancy;
+    ctas = std::min<int64_t>(
+        ctas, int64_t(current_sms()) *
+                  occupancy.get(reinterpret_cast<const void*>(fn), kRouteWarps * 32, smem));
+  }
+  return launch("fs_route", fn, dim3(static_cast<unsigned>(ctas)), kRouteWarps * 32, smem, st, 1,
+                P);
 }
 
 fs_status route(const fs_matrix* z, const fs_route_options* o, float* weights, int32_t* ids,
@@ -211,23 +234,15 @@ fs_status route(const fs_matrix* z, const fs_route_options* o, float* weights, i
   P.weights = weights;
   P.ids = ids;
   P.load = load;
-  // one warp per row; with a load to count, CTAs stay and take several rows each, so that few
-  // histograms are added up
-  int64_t ctas = (z->rows + kRouteWarps - 1) / kRouteWarps;
-  if (load) ctas = std::min<int64_t>(ctas, 8ll * current_sms());
-  const size_t smem = static_cast<size_t>(P.experts) * (kRouteWarps * sizeof(double) + sizeof(int));
+  const int64_t ctas = (z->rows + kRouteWarps - 1) / kRouteWarps;  // one warp per row
+  const size_t smem = static_cast<size_t>(route_room(P.experts)) * kRouteWarps * sizeof(double) +
+                      P.experts * sizeof(int);
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
     return by_width(z->cols, [&](auto nl) -> fs_status {
-      constexpr auto fn = route_kernel<T, decltype(nl)::value>;
-      static PerDeviceOnce once;
-      const fs_status a = once.run("cudaFuncSetAttribute", [&] {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    FS_MAX_EXPERTS * (kRouteWarps * 8 + 4));
-      });
-      if (a != FS_OK) return a;
-      return launch("fs_route", fn, dim3(static_cast<unsigned>(ctas)), kRouteWarps * 32, smem, st,
-                    1, P);
+      constexpr int NL = decltype(nl)::value;
+      return o->score == FS_SCORE_SIGMOID ? launch_route<T, NL, true>(P, ctas, smem, st)
+                                          : launch_route<T, NL, false>(P, ctas, smem, st);
     });
   });
 }
