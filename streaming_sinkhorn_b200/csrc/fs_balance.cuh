@@ -8,15 +8,19 @@
 //   e_ij = 2^(u_ij + gamma_j - m_i),  S_i = sum_j e_ij,  phi_i = -(m_i + log2(S_i / E)),
 //   c_j = mean_i e_ij E / S_i,        gamma_j <- gamma_j - log2 c_j + log2 beta_j,
 // since 2^(u_ij + phi_i) = e_ij (E / S_i) 2^-gamma_j. Means and not sums with the logarithm of
-// a weight: those would cancel. A column whose c_j comes out below 2^-100 (its terms may have
+// a weight: those would cancel. A column whose c_j comes out below 2^-40 (its terms may have
 // been flushed) is done over with its own maximum.
 //
 // One launch does all iterations. Every CTA keeps its rows' u in shared memory in fp32 (the
-// rest, if they do not all fit, in the workspace, read through L2), a group of lanes takes a
-// row, each lane holding the column sums of its columns in registers; per iteration the CTAs
-// exchange one row of column sums each and meet at a grid barrier. The launch is cooperative,
-// so all CTAs run at once, and every wait is bounded: when one expires the call's outputs are
-// NaN.
+// rest, if they do not all fit, in the workspace, read through L2 one step ahead), a group of
+// lanes takes a row, two rows at a time, each lane holding the column sums of its columns in
+// registers. All rows of a CTA share one offset in place of m_i, the largest u of the CTA plus
+// the largest gamma, so a row needs one reduction; a row whose sum comes out below 2^-60 is done
+// over with its own maximum. Per iteration the CTAs exchange one row of column sums each:
+// through distributed shared memory in a cluster of up to 16 CTAs when the whole problem fits
+// into their shared memory, else through the workspace and a grid barrier. That launch is
+// cooperative, so all CTAs run at once, and its waits are bounded: when one expires the call's
+// outputs are NaN.
 #pragma once
 
 #include "fs_rowload.cuh"
@@ -24,9 +28,11 @@
 
 namespace fs {
 
-constexpr int kBalThreads = 512;
-constexpr int kBalWarps = kBalThreads / 32;
-constexpr float kBalFlushed = 0x1p-100f;
+constexpr int kBalClusterWarps = 16;
+constexpr int kBalGridWarps = 32;
+constexpr int kBalMaxCluster = 16;
+constexpr float kBalLowSum = 0x1p-60f;   // a row's sum that may have lost terms
+constexpr float kBalFlushed = 0x1p-40f;  // a column's mean that may have lost terms
 
 struct BalanceParams {
   const void* z;
@@ -44,7 +50,7 @@ struct BalanceParams {
   float* f;
   float* g;
   unsigned* sync;   // [0] arrivals, [1] nonzero once a wait has expired; zeroed before the launch
-  float* part;      // [2][gridDim][cols + 1] column sums (and open rows) by iteration parity
+  float* part;      // [2][gridDim][cols + 4] column sums (and open rows) by iteration parity
   float2* redo;     // [gridDim][cols] (max, sum) of columns done over
   float* spill;     // u of the rows beyond `resident`, (gridDim, per_cta - resident, cols)
 };
@@ -77,11 +83,12 @@ __device__ __forceinline__ bool grid_barrier(unsigned* sync, unsigned target, in
 
 // Lane l of the LPT lanes of a row holds columns 4 (LPT q + l) .. + 3 for q = 0 .. NL / 4 - 1:
 // 16-byte accesses of neighbouring lanes are neighbours in memory.
-template <int NL, int LPT>
+template <int NL, int LPT, int NW>
 struct BalShape {
+  static constexpr int kThreads = NW * 32;
   static constexpr int kCols = NL * LPT;
   static constexpr int kGroups = 32 / LPT;               // rows a warp takes at once
-  static constexpr int kRowStep = kGroups * kBalWarps;   // rows a CTA takes at once
+  static constexpr int kRowStep = kGroups * NW;          // rows a CTA takes at once
   static __host__ __device__ constexpr int column(int l, int i) {
     return 4 * (LPT * (i / 4) + l) + i % 4;
   }
@@ -100,17 +107,111 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-template <typename T, int NL, int LPT>
-__global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceParams P) {
-  using S = BalShape<NL, LPT>;
+// The exponentials e_i = 2^(u_i + g_i) of H rows over this lane's columns and their sums over
+// the rows; g holds gamma less the offset. A sum too low for comfort is taken again about the
+// row's own maximum, which `extra` returns (0 otherwise). Called by whole warps.
+template <int NL, int LPT, int H>
+__device__ __forceinline__ void bal_rows(const float4 (*u)[NL / 4], const float* g, float (*e)[NL],
+                                         float* sum, float* extra) {
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    u64 acc = pk(0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < NL / 4; ++q) {
+      const float4 x = u[h][q];
+      float t0, t1, t2, t3;
+      upk(add2(pk(x.x, x.y), pk(g[4 * q], g[4 * q + 1])), t0, t1);
+      upk(add2(pk(x.z, x.w), pk(g[4 * q + 2], g[4 * q + 3])), t2, t3);
+      e[h][4 * q] = ex2(t0);
+      e[h][4 * q + 1] = ex2(t1);
+      e[h][4 * q + 2] = ex2(t2);
+      e[h][4 * q + 3] = ex2(t3);
+      acc = add2(acc, add2(pk(e[h][4 * q], e[h][4 * q + 1]), pk(e[h][4 * q + 2], e[h][4 * q + 3])));
+    }
+    float x, y;
+    upk(acc, x, y);
+    sum[h] = x + y;
+    extra[h] = 0.0f;
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) sum[h] = group_sum<LPT>(sum[h]);
+  bool any = sum[0] < kBalLowSum;
+  if (H == 2) any |= sum[H - 1] < kBalLowSum;
+  if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < NL / 4; ++q) {
+        m = fmaxf(m, fmaxf(u[h][q].x + g[4 * q], u[h][q].y + g[4 * q + 1]));
+        m = fmaxf(m, fmaxf(u[h][q].z + g[4 * q + 2], u[h][q].w + g[4 * q + 3]));
+      }
+      m = group_max<LPT>(m);
+      const bool low = sum[h] < kBalLowSum && m != -INFINITY;  // (no open column: 0)
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < NL / 4; ++q) {
+        const float t[4] = {u[h][q].x + g[4 * q], u[h][q].y + g[4 * q + 1], u[h][q].z + g[4 * q + 2],
+                            u[h][q].w + g[4 * q + 3]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (low) e[h][4 * q + i] = ex2(t[i] - m);
+          s += e[h][4 * q + i];
+        }
+      }
+      s = group_sum<LPT>(s);
+      if (low) {
+        sum[h] = s;
+        extra[h] = m;
+      }
+    }
+  }
+}
+
+// Four neighbouring logits of a row, -inf beyond the last.
+template <typename T>
+__device__ __forceinline__ float4 bal_load(const T* z, int j, int E, bool vec) {
+  if (vec && j < E) {
+    if constexpr (sizeof(T) == 4) {
+      return *reinterpret_cast<const float4*>(z + j);
+    } else {
+      const uint2 r = *reinterpret_cast<const uint2*>(z + j);
+      float f[8];
+      Elem<T>::unpack(make_uint4(r.x, r.y, 0u, 0u), f);
+      return make_float4(f[0], f[1], f[2], f[3]);
+    }
+  }
+  return make_float4(j < E ? Elem<T>::to_f(z[j]) : -INFINITY,
+                     j + 1 < E ? Elem<T>::to_f(z[j + 1]) : -INFINITY,
+                     j + 2 < E ? Elem<T>::to_f(z[j + 2]) : -INFINITY,
+                     j + 3 < E ? Elem<T>::to_f(z[j + 3]) : -INFINITY);
+}
+
+// log2 of a positive float in two parts, so that a large offset meets the whole number first.
+__device__ __forceinline__ float bal_log2(float v, float offset) {
+  int k;
+  const float f = frexpf(v, &k);
+  return (offset + static_cast<float>(k)) + log2f(f);
+}
+
+template <typename T, int NL, int LPT, int NW, bool CLUSTER>
+__global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams P) {
+  using S = BalShape<NL, LPT, NW>;
+  constexpr int kPartCols = S::kCols + 4;  // column sums, then the open rows
+  constexpr int kQuads = S::kCols / 4;
+  constexpr int kParts = kQuads >= S::kThreads ? 1 : (S::kThreads / kQuads < NW
+                                                          ? S::kThreads / kQuads
+                                                          : NW);
   extern __shared__ __align__(16) float bal_smem[];
   __shared__ int ok_sh;
-  __shared__ float open_sh[kBalWarps];
+  __shared__ float warp_sh[2][NW];
+  __shared__ uint64_t part_bar[2];  // CLUSTER: all CTAs' sums have arrived (by parity)
   __shared__ int redo_sh;
   float* gam = bal_smem;              // [cols] gamma
   float* lb = gam + S::kCols;         // [cols] log2 beta
-  float* csum = lb + S::kCols;        // [max(kBalWarps, threads / cols)][cols] partial sums
-  float* u_res = csum + kBalWarps * S::kCols;
+  float* csum = lb + S::kCols;        // [NW][cols] partial sums
+  float* parts = csum + NW * S::kCols;  // CLUSTER: [2][16][kPartCols]
+  float* u_res = parts + (CLUSTER ? 2 * kBalMaxCluster * kPartCols : 0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int l = lane % LPT, grp = lane / LPT;
   const int E = P.experts;
@@ -121,6 +222,11 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
   float* u_spill = P.spill + static_cast<int64_t>(blockIdx.x) * (P.per_cta - P.resident) * S::kCols;
   const int G = gridDim.x;
   unsigned arrivals = 0;
+  // (generic addressing: resident rows lie in shared memory, the rest in the workspace)
+  auto row_of = [&](int r) -> float* {
+    return r < P.resident ? u_res + static_cast<int64_t>(r) * S::kCols
+                          : u_spill + static_cast<int64_t>(r - P.resident) * S::kCols;
+  };
 
   // log2 beta, gamma of the start
   if (warp == 0) {
@@ -139,20 +245,35 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
     }
   }
 
-  // u of the CTA's rows; rows without an open column are counted out
+  // u of the CTA's rows and the largest of them; rows without an open column are counted out
   int open = 0;
+  float umax = -INFINITY;
+  const T* z0 = static_cast<const T*>(P.z) + row0 * P.ld;
+  const bool vec = E % 4 == 0 && P.ld % 4 == 0 &&
+                   (reinterpret_cast<uintptr_t>(P.z) & (4 * sizeof(T) - 1)) == 0;
+  float4 ahead[NL / 4];
+  auto read = [&](int b) {
+    const int r = b + grp < n ? b + grp : n - 1;
+#pragma unroll
+    for (int q = 0; q < NL / 4; ++q)
+      ahead[q] = bal_load(z0 + static_cast<int64_t>(r) * P.ld, S::column(l, 4 * q), E, vec);
+  };
+  if (warp * S::kGroups < n) read(warp * S::kGroups);
   for (int b = warp * S::kGroups; b < n; b += S::kRowStep) {
     const int r = b + grp;
     const bool have = r < n;
-    const T* z = static_cast<const T*>(P.z) + (row0 + (have ? r : 0)) * P.ld;
     float v[NL];
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int j = S::column(l, i);
-      v[i] = have && j < E ? Elem<T>::to_f(z[j]) : -INFINITY;
-      m = fmaxf(m, v[i]);
+    for (int q = 0; q < NL / 4; ++q) {
+      v[4 * q] = have ? ahead[q].x : -INFINITY;
+      v[4 * q + 1] = have ? ahead[q].y : -INFINITY;
+      v[4 * q + 2] = have ? ahead[q].z : -INFINITY;
+      v[4 * q + 3] = have ? ahead[q].w : -INFINITY;
     }
+    if (b + S::kRowStep < n) read(b + S::kRowStep);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) m = fmaxf(m, v[i]);
     if (P.score == kScoreSoftmax) {
       m = group_max<LPT>(m);
       const float mm = m == -INFINITY ? 0.0f : m;
@@ -172,64 +293,105 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
         v[i] = v[i] == -INFINITY ? -INFINITY : route_score(v[i], kScoreSigmoid, 0.0f, 0.0f) * ke;
       m = group_max<LPT>(m);
     }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) umax = fmaxf(umax, v[i]);
     // (a row of NaN is open: its NaN reaches every output)
     if (have && l == 0 && m != -INFINITY) ++open;
     if (have) {
-      float* dst = r < P.resident ? u_res + static_cast<int64_t>(r) * S::kCols
-                                  : u_spill + static_cast<int64_t>(r - P.resident) * S::kCols;
+      float4* dst = reinterpret_cast<float4*>(row_of(r));
 #pragma unroll
       for (int q = 0; q < NL / 4; ++q)
-        reinterpret_cast<float4*>(dst)[LPT * q + l] =
-            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        dst[LPT * q + l] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
     }
   }
   open = __reduce_add_sync(0xffffffffu, open);
-  if (lane == 0) open_sh[warp] = static_cast<float>(open);
+  umax = warp_maxf(umax);
+  if (lane == 0) {
+    warp_sh[0][warp] = static_cast<float>(open);
+    warp_sh[1][warp] = umax;
+  }
   __syncthreads();
+  umax = warp_maxf(lane < NW ? warp_sh[1][lane] : -INFINITY);
+  if (umax == -INFINITY) umax = 0.0f;
 
-  double open_rows = 0.0;
+  if (CLUSTER && G > 1) {
+    if (tid == 0) {
+      mbar_init(&part_bar[0], 1);
+      mbar_init(&part_bar[1], 1);
+      fence_mbar_init();
+    }
+    cluster_barrier();  // no CTA writes into another's shared memory before that one is ready
+  }
+
+  float open_rows = 0.0f;
   bool alive = true;
   for (int it = 0; it < P.n_iters && alive; ++it) {
     const bool last = it == P.n_iters - 1;
     float gm[NL], acc[NL];
+    float off = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       gm[i] = gam[S::column(l, i)];
+      off = fmaxf(off, gm[i]);
       acc[i] = 0.0f;
     }
-    for (int b = warp * S::kGroups; b < n; b += S::kRowStep) {
-      const int r = b + grp;
-      const bool have = r < n;
-      const int rr = have ? r : b;
-      const float* src = rr < P.resident ? u_res + static_cast<int64_t>(rr) * S::kCols
-                                         : u_spill + static_cast<int64_t>(rr - P.resident) * S::kCols;
-      float t[NL];
-      float m = -INFINITY;
+    off = group_max<LPT>(off);
+    off = (off == -INFINITY ? 0.0f : off) + umax;
 #pragma unroll
-      for (int q = 0; q < NL / 4; ++q) {
-        const float4 x = reinterpret_cast<const float4*>(src)[LPT * q + l];
-        t[4 * q] = x.x + gm[4 * q];
-        t[4 * q + 1] = x.y + gm[4 * q + 1];
-        t[4 * q + 2] = x.z + gm[4 * q + 2];
-        t[4 * q + 3] = x.w + gm[4 * q + 3];
-        m = max3(m, t[4 * q], t[4 * q + 1]);
-        m = max3(m, t[4 * q + 2], t[4 * q + 3]);
+    for (int i = 0; i < NL; ++i) gm[i] -= off;
+    // Rows are read one step ahead; with 16 warps two rows a step (b + grp and the next
+    // group's). More than 256 columns leave no registers for either.
+    constexpr int kH = NL == 8 && NW == 16 ? 2 : 1;
+    constexpr bool kAhead = NL == 8;
+    constexpr int kStep = kH * S::kRowStep;
+    float4 nx[kH][NL / 4];
+    auto fetch = [&](int b) {
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+        const int r = b + h * S::kGroups + grp;
+        if (r < P.resident && r < n) {
+          const float4* src = reinterpret_cast<const float4*>(u_res + static_cast<int64_t>(r) * S::kCols);
+#pragma unroll
+          for (int q = 0; q < NL / 4; ++q) nx[h][q] = src[LPT * q + l];
+        } else if (r < n) {
+          const float4* src = reinterpret_cast<const float4*>(
+              u_spill + static_cast<int64_t>(r - P.resident) * S::kCols);
+#pragma unroll
+          for (int q = 0; q < NL / 4; ++q) nx[h][q] = __ldcg(src + LPT * q + l);
+        } else {
+#pragma unroll
+          for (int q = 0; q < NL / 4; ++q)
+            nx[h][q] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
       }
-      m = group_max<LPT>(m);
-      const bool empty = m == -INFINITY;  // no open column (or only NaN, which the sum keeps)
-      const float mm = empty ? 0.0f : m;
-      float sum = 0.0f;
+    };
+    const int b0 = warp * kH * S::kGroups;
+    if (kAhead && b0 < n) fetch(b0);
+    for (int b = b0; b < n; b += kStep) {
+      if (!kAhead) fetch(b);
+      float4 u[kH][NL / 4];
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        t[i] = ex2(t[i] - mm);
-        sum += t[i];
+      for (int h = 0; h < kH; ++h)
+#pragma unroll
+        for (int q = 0; q < NL / 4; ++q) u[h][q] = nx[h][q];
+      if (kAhead && b + kStep < n) fetch(b + kStep);
+      float e[kH][NL], sum[kH], extra[kH];
+      bal_rows<NL, LPT, kH>(u, gm, e, sum, extra);
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+        const int r = b + h * S::kGroups + grp;
+        const float w = sum[h] == 0.0f ? 0.0f : __fdividef(static_cast<float>(E), sum[h]);
+        const u64 w2 = pk(w, w);
+#pragma unroll
+        for (int i = 0; i < NL; i += 2) {
+          const u64 a = fma2(pk(e[h][i], e[h][i + 1]), w2, pk(acc[i], acc[i + 1]));
+          upk(a, acc[i], acc[i + 1]);
+        }
+        if (last && r < n && l == 0)
+          P.f[row0 + r] =
+              sum[h] == 0.0f ? 0.0f
+                             : -bal_log2(sum[h] / static_cast<float>(E), off + extra[h]) / ke;
       }
-      sum = group_sum<LPT>(sum);
-      const float w = !have || sum == 0.0f ? 0.0f : static_cast<float>(E) / sum;
-#pragma unroll
-      for (int i = 0; i < NL; ++i) acc[i] = fmaf(t[i], w, acc[i]);
-      if (last && have && l == 0)
-        P.f[row0 + r] = sum == 0.0f ? 0.0f : -(mm + log2f(sum / static_cast<float>(E))) / ke;
     }
     // the CTA's column sums: rows of a warp, then the warps in their order
 #pragma unroll
@@ -238,64 +400,102 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
       for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
       if (grp == 0) csum[warp * S::kCols + S::column(l, i)] = acc[i];
     }
+    if (tid == 0) redo_sh = 0;
     __syncthreads();
-    float* part = P.part + static_cast<int64_t>(it & 1) * G * (S::kCols + 1);
-    for (int j = tid; j < S::kCols; j += kBalThreads) {
+    if constexpr (CLUSTER) {
+      // every column's sum to every CTA, counted on its barrier of this parity. (A CTA two
+      // iterations ahead cannot be: it waits for this one's sums in between.)
+      float* part = parts + (it & 1) * kBalMaxCluster * kPartCols;
+      uint64_t* bar = &part_bar[it & 1];
+      constexpr int kAtOnce = S::kThreads / S::kCols;  // CTAs written to at a time
+      const int j = tid % S::kCols;
       float c = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) c += csum[w * S::kCols + j];
-      part[static_cast<int64_t>(blockIdx.x) * (S::kCols + 1) + j] = c;
-    }
-    if (tid == 0) {
-      float c = 0.0f;
-      for (int w = 0; w < kBalWarps; ++w) c += open_sh[w];
-      part[static_cast<int64_t>(blockIdx.x) * (S::kCols + 1) + S::kCols] = c;
-      redo_sh = 0;
-    }
-    arrivals += G;
-    alive = grid_barrier(P.sync, arrivals, &ok_sh);
-    if (!alive) break;
-    if (it == 0) {
-      for (int q = 0; q < G; ++q)
-        open_rows += __ldcg(part + static_cast<int64_t>(q) * (S::kCols + 1) + S::kCols);
-      open_rows = fmax(open_rows, 1.0);  // (no open row at all: f = g = 0)
-    }
-    // every CTA adds all CTAs' sums in the same order
-    constexpr int kParts = S::kCols >= kBalThreads ? 1 : (kBalThreads / S::kCols < kBalWarps
-                                                              ? kBalThreads / S::kCols
-                                                              : kBalWarps);
-    for (int w = tid; w < kParts * S::kCols; w += kBalThreads) {
-      const int j = w % S::kCols, pt = w / S::kCols;
-      float c = 0.0f;
-#pragma unroll 8
-      for (int q = pt; q < G; q += kParts)
-        c += __ldcg(part + static_cast<int64_t>(q) * (S::kCols + 1) + j);
-      csum[w] = c;
-    }
-    __syncthreads();
-    for (int j = tid; j < E; j += kBalThreads) {
-      float c = 0.0f;
+      for (int w = 0; w < NW; ++w) c += csum[w * S::kCols + j];
+      float o = 0.0f;
+      if (it == 0 && tid < G)
+        for (int w = 0; w < NW; ++w) o += warp_sh[0][w];
+      if (G == 1) {  // (a launch without a cluster: nothing to exchange)
+        if (tid < S::kCols) part[j] = c;
+        if (it == 0 && tid == 0) part[S::kCols] = o;
+        __syncthreads();
+      } else {
+        if (tid == 0)
+          mbar_expect_tx(bar, static_cast<uint32_t>(G) * (S::kCols + (it == 0 ? 1 : 0)) * 4u);
+        for (int q = tid / S::kCols; q < G; q += kAtOnce)
+          st_async_cluster(part + blockIdx.x * kPartCols + j, q, c, bar);
+        if (it == 0 && tid < G)
+          st_async_cluster(part + blockIdx.x * kPartCols + S::kCols, tid, o, bar);
+        const bool ok = mbar_wait_cluster_bounded(bar, static_cast<uint32_t>(it >> 1) & 1u);
+        if (__syncthreads_or(!ok)) {
+          alive = false;
+          break;
+        }
+      }
+      if (it == 0) {
+        for (int q = 0; q < G; ++q) open_rows += part[q * kPartCols + S::kCols];
+        open_rows = fmaxf(open_rows, 1.0f);  // (no open row at all: f = g = 0)
+      }
+    } else {
+      float* part = P.part + static_cast<int64_t>(it & 1) * G * kPartCols;
+      for (int j = tid; j <= S::kCols; j += S::kThreads) {
+        float c = 0.0f;
 #pragma unroll
-      for (int pt = 0; pt < kParts; ++pt) c += csum[pt * S::kCols + j];
-      c = static_cast<float>(c / open_rows);
+        for (int w = 0; w < NW; ++w) c += j < S::kCols ? csum[w * S::kCols + j] : warp_sh[0][w];
+        part[static_cast<int64_t>(blockIdx.x) * kPartCols + j] = c;
+      }
+      arrivals += G;
+      alive = grid_barrier(P.sync, arrivals, &ok_sh);
+      if (!alive) break;
+      if (it == 0) {
+        double o = 0.0;
+        for (int q = 0; q < G; ++q)
+          o += __ldcg(part + static_cast<int64_t>(q) * kPartCols + S::kCols);
+        open_rows = static_cast<float>(fmax(o, 1.0));
+      }
+      // every CTA adds all CTAs' sums in the same order: four columns a thread, kParts strided
+      // parts of the CTAs, then (below) the parts
+      for (int w = tid; w < kParts * kQuads; w += S::kThreads) {
+        const int j = w % kQuads, pt = w / kQuads;
+        float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 10
+        for (int q = pt; q < G; q += kParts) {
+          const float4 x = __ldcg(
+              reinterpret_cast<const float4*>(part + static_cast<int64_t>(q) * kPartCols) + j);
+          c = make_float4(c.x + x.x, c.y + x.y, c.z + x.z, c.w + x.w);
+        }
+        reinterpret_cast<float4*>(csum)[w] = c;
+      }
+      __syncthreads();
+    }
+    for (int j = tid; j < E; j += S::kThreads) {
+      float c = 0.0f;
+      if constexpr (CLUSTER) {
+        const float* part = parts + (it & 1) * kBalMaxCluster * kPartCols + j;
+        for (int q = 0; q < G; ++q) c += part[q * kPartCols];
+      } else {
+#pragma unroll
+        for (int pt = 0; pt < kParts; ++pt) c += csum[pt * S::kCols + j];
+      }
+      c /= open_rows;
       csum[j] = c;  // (each thread rewrites only what it alone has read: part 0 of its column)
       if (lb[j] == -INFINITY) {
         gam[j] = -INFINITY;  // nothing is wanted of this column
       } else if (c < kBalFlushed) {
         redo_sh = 1;
       } else {
-        gam[j] = gam[j] - log2f(c) + lb[j];
+        // the gamma that the rows have seen is the rounded one less the offset
+        gam[j] = ((gam[j] - off) + off) - log2f(c) + lb[j];
       }
     }
     __syncthreads();
     if (redo_sh) {  // the same in every CTA: all have the same sums
       // columns done over in their own range: max and sum of u_ij + phi_i over the rows
-      for (int j = tid; j < E; j += kBalThreads) {
+      for (int j = tid; j < E; j += S::kThreads) {
         if (lb[j] == -INFINITY || !(csum[j] < kBalFlushed)) continue;
         float cm = -INFINITY, cl = 0.0f;
         for (int r = 0; r < n; ++r) {
-          const float* src = r < P.resident ? u_res + static_cast<int64_t>(r) * S::kCols
-                                            : u_spill + static_cast<int64_t>(r - P.resident) * S::kCols;
+          const float* src = row_of(r);
           // phi_i again, from the gammas the rows have seen: gamma + what this update added
           float m = -INFINITY;
           for (int k = 0; k < E; ++k) {
@@ -320,10 +520,16 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
         }
         P.redo[static_cast<int64_t>(blockIdx.x) * S::kCols + j] = make_float2(cm, cl);
       }
-      arrivals += G;
-      alive = grid_barrier(P.sync, arrivals, &ok_sh);
-      if (!alive) break;
-      for (int j = tid; j < E; j += kBalThreads) {
+      if constexpr (CLUSTER) {
+        __threadfence();
+        if (G > 1) cluster_barrier();
+        __syncthreads();
+      } else {
+        arrivals += G;
+        alive = grid_barrier(P.sync, arrivals, &ok_sh);
+        if (!alive) break;
+      }
+      for (int j = tid; j < E; j += S::kThreads) {
         if (lb[j] == -INFINITY || !(csum[j] < kBalFlushed)) continue;
         float cm = -INFINITY, cl = 0.0f;
         for (int q = 0; q < G; ++q) {
@@ -335,19 +541,20 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalancePa
         }
         // a column closed to every row keeps g = 0
         gam[j] = cm == -INFINITY ? lb[j]
-                                 : -(cm + log2f(static_cast<float>(cl / open_rows))) + lb[j];
+                                 : -(cm + log2f(cl / open_rows)) + lb[j];
       }
       __syncthreads();
     }
   }
+  if (CLUSTER && G > 1) cluster_barrier();  // no CTA leaves while sums are on their way to it
   if (!alive) {
-    for (int r = tid; r < n; r += kBalThreads) P.f[row0 + r] = __int_as_float(0x7FC00000);
+    for (int r = tid; r < n; r += S::kThreads) P.f[row0 + r] = __int_as_float(0x7FC00000);
     if (blockIdx.x == 0)
-      for (int j = tid; j < E; j += kBalThreads) P.g[j] = __int_as_float(0x7FC00000);
+      for (int j = tid; j < E; j += S::kThreads) P.g[j] = __int_as_float(0x7FC00000);
     return;
   }
   if (blockIdx.x == 0)
-    for (int j = tid; j < E; j += kBalThreads)
+    for (int j = tid; j < E; j += S::kThreads)
       P.g[j] = lb[j] == -INFINITY ? -INFINITY : (gam[j] - lb[j]) / ke;
 }
 

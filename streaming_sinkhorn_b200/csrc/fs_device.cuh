@@ -178,6 +178,47 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// ---- clusters ------------------------------------------------------------------------------
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Stores v at the address of `local` in the shared memory of CTA `rank` of the cluster and
+// counts its 4 bytes on that CTA's mbarrier at the address of `bar` (asynchronous store).
+__device__ __forceinline__ void st_async_cluster(float* local, unsigned rank, float v,
+                                                 uint64_t* bar) {
+  uint32_t ra, rb;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)),
+               "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)),
+               "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   ra),
+               "r"(__float_as_uint(v)), "r"(rb)
+               : "memory");
+}
+
+// Bounded wait for a phase of an mbarrier that other CTAs of the cluster complete, with
+// acquire semantics at cluster scope (their stores are then visible here).
+__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done) return true;
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
 // ---- reductions -----------------------------------------------------------------------------
 
 __device__ __forceinline__ double warp_sum(double v) {

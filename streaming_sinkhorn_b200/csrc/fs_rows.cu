@@ -283,33 +283,54 @@ fs_status route_grad(const fs_matrix* z, const fs_route_options* o, const float*
 
 // The launch of one problem: lanes per row, CTAs, and what fits in shared memory.
 struct BalancePlan {
-  int nl, lpt, cols;
+  int nl, lpt, nw, cols;
+  bool cluster;  // one cluster, everything in shared memory
   int ctas, per_cta, resident;
   size_t smem;
   size_t off_redo, off_spill, total;  // workspace: sync word, partial sums, redo, spill
 };
 
-constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 80 bytes
+constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 140 bytes
 
-BalancePlan balance_plan(int64_t rows, int64_t experts) {
+BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   BalancePlan p{};
   p.nl = experts <= 256 ? 8 : experts <= 512 ? 16 : 32;
   p.lpt = 1;
   while (p.nl * p.lpt < experts) p.lpt *= 2;
   p.cols = p.nl * p.lpt;
-  // rows a CTA takes at once; a grid barrier costs as much as a few such steps
-  const int64_t step = (32 / p.lpt) * kBalWarps;
-  const int64_t want = (rows + 2 * step - 1) / (2 * step);
-  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(want, current_sms()));
-  const int64_t per = std::max<int64_t>(1, (rows + ctas - 1) / ctas);
-  p.per_cta = static_cast<int>(per);
-  p.ctas = static_cast<int>(std::max<int64_t>(1, (rows + per - 1) / per));
-  const size_t fixed = static_cast<size_t>(2 + kBalWarps) * p.cols * 4;
+  const size_t cluster_fixed =
+      static_cast<size_t>(2 + kBalClusterWarps) * p.cols * 4 + 2ull * kBalMaxCluster * (p.cols + 4) * 4;
   const size_t row = static_cast<size_t>(p.cols) * 4;
-  p.resident = static_cast<int>(std::min<int64_t>(per, (kBalSmemBudget - fixed) / row));
-  p.smem = fixed + p.resident * row;
+  const int64_t step = (32 / p.lpt) * kBalClusterWarps;  // rows a CTA takes at once
+  auto spread = [&](int64_t ctas) {
+    const int64_t per = std::max<int64_t>(1, (rows + ctas - 1) / ctas);
+    p.per_cta = static_cast<int>(per);
+    p.ctas = static_cast<int>(std::max<int64_t>(1, (rows + per - 1) / per));
+  };
+  // A cluster exchanges sums in well under a microsecond, a grid barrier takes about three
+  // (8191 x 64, 10 iterations: 39 us on the grid), so a cluster is taken whenever its shared
+  // memory holds the problem; with fewer rows, fewer CTAs of it.
+  p.cluster = false;
+  if (allow_cluster && p.nl == 8) {
+    for (int c = 1; c <= kBalMaxCluster && !p.cluster; c *= 2) {
+      if (c < kBalMaxCluster && rows > 2 * step * c) continue;
+      if ((rows + c - 1) / c * row + cluster_fixed > kBalSmemBudget) continue;
+      p.cluster = true;
+      // (a cluster launch wants all of its CTAs, empty ones too)
+      p.per_cta = static_cast<int>(std::max<int64_t>(1, (rows + c - 1) / c));
+      p.ctas = c;
+    }
+  }
+  if (!p.cluster)
+    spread(std::max<int64_t>(1, std::min<int64_t>((rows + 2 * step - 1) / (2 * step), current_sms())));
+  // The grid's CTAs have many rows each and hide their latencies with more warps, where the
+  // registers allow it.
+  p.nw = p.cluster || p.nl > 8 ? kBalClusterWarps : kBalGridWarps;
+  const size_t used = p.cluster ? cluster_fixed : static_cast<size_t>(2 + p.nw) * p.cols * 4;
+  p.resident = static_cast<int>(std::min<int64_t>(p.per_cta, (kBalSmemBudget - used) / row));
+  p.smem = used + p.resident * row;
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
-  p.off_redo = 256 + up(2 * static_cast<size_t>(p.ctas) * (p.cols + 1) * 4);
+  p.off_redo = 256 + up(2 * static_cast<size_t>(p.ctas) * (p.cols + 4) * 4);
   p.off_spill = p.off_redo + up(static_cast<size_t>(p.ctas) * p.cols * 8);
   p.total = p.off_spill + up(static_cast<size_t>(p.ctas) * (p.per_cta - p.resident) * row);
   return p;
@@ -336,6 +357,54 @@ fs_status by_shape(const BalancePlan& p, F&& f) {
   }
 }
 
+// Whether the current device can run a cluster of 16 CTAs with all of the shared memory (asked
+// once per device, of one of the kernels: all have the same block and budget).
+bool cluster_runs() {
+  static std::atomic<int> known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    constexpr auto fn = balance_kernel<float, 8, 8, kBalClusterWarps, true>;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kBalMaxCluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(kBalMaxCluster);
+    cfg.blockDim = dim3(kBalClusterWarps * 32);
+    cfg.dynamicSmemBytes = kBalSmemBudget;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kBalSmemBudget)) == cudaSuccess &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+    cudaGetLastError();
+    k = ok ? 1 : -1;
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k > 0;
+}
+
+template <typename T, int NL, int LPT, int NW, bool CLUSTER>
+fs_status launch_balance(const BalanceParams& P, const BalancePlan& p, cudaStream_t st) {
+  constexpr auto fn = balance_kernel<T, NL, LPT, NW, CLUSTER>;
+  static PerDeviceOnce once;
+  const fs_status s = once.run("cudaFuncSetAttribute", [&] {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kBalSmemBudget));
+    if (e != cudaSuccess || !CLUSTER) return e;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (s != FS_OK) return s;
+  return launch("fs_balance", fn, dim3(static_cast<unsigned>(p.ctas)), NW * 32, p.smem, st,
+                CLUSTER ? p.ctas : kCooperative, P);
+}
+
 fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters, const float* load,
                   const float* g_init, float* f, float* g, void* ws, size_t ws_bytes,
                   cudaStream_t st) {
@@ -348,7 +417,8 @@ fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
   if (!f || !g) return FS_ERR_NULL;
   if (!aligned(load, 4) || !aligned(g_init, 4) || !aligned(f, 4) || !aligned(g, 4))
     return FS_ERR_ALIGNMENT;
-  const BalancePlan p = balance_plan(z->rows, z->cols);
+  BalancePlan p = balance_plan(z->rows, z->cols, true);
+  if (p.cluster && !cluster_runs()) p = balance_plan(z->rows, z->cols, false);
   if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
   unsigned char* base = static_cast<unsigned char*>(ws);
   BalanceParams P{};
@@ -370,20 +440,17 @@ fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
   P.part = reinterpret_cast<float*>(base + 256);
   P.redo = reinterpret_cast<float2*>(base + p.off_redo);
   P.spill = reinterpret_cast<float*>(base + p.off_spill);
-  s = cuda_status(cudaMemsetAsync(base, 0, 256, st), "cudaMemsetAsync");
-  if (s != FS_OK) return s;
+  if (!p.cluster) {  // the grid barrier's word
+    s = cuda_status(cudaMemsetAsync(base, 0, 256, st), "cudaMemsetAsync");
+    if (s != FS_OK) return s;
+  }
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
     return by_shape(p, [&](auto nl, auto lpt) -> fs_status {
-      constexpr auto fn = balance_kernel<T, decltype(nl)::value, decltype(lpt)::value>;
-      static PerDeviceOnce once;
-      const fs_status a = once.run("cudaFuncSetAttribute", [&] {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kBalSmemBudget));
-      });
-      if (a != FS_OK) return a;
-      return launch("fs_balance", fn, dim3(static_cast<unsigned>(p.ctas)), kBalThreads, p.smem, st,
-                    kCooperative, P);
+      constexpr int NL = decltype(nl)::value, LPT = decltype(lpt)::value;
+      if constexpr (NL == 8)
+        if (p.cluster) return launch_balance<T, NL, LPT, kBalClusterWarps, true>(P, p, st);
+      return launch_balance<T, NL, LPT, NL == 8 ? kBalGridWarps : kBalClusterWarps, false>(P, p, st);
     });
   });
 }
@@ -425,7 +492,8 @@ fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt, const f
 size_t fs_balance_workspace_bytes(const fs_matrix* z) {
   if (!z || z->rows < 0 || z->rows > fs::kMaxInt || z->cols < 1 || z->cols > FS_MAX_EXPERTS)
     return 0;
-  return fs::balance_plan(z->rows, z->cols).total;
+  return std::max(fs::balance_plan(z->rows, z->cols, true).total,
+                  fs::balance_plan(z->rows, z->cols, false).total);
 }
 
 fs_status fs_balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,

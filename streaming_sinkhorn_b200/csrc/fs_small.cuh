@@ -56,12 +56,6 @@ struct SmallParams {
   unsigned* err;        // the workspace error word (a wait that timed out sets kErrTimeout)
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -79,39 +73,6 @@ __device__ __forceinline__ unsigned cluster_size() {
 __host__ __device__ inline size_t small_smem_bytes(int64_t n, int64_t m, int D) {
   const int64_t np = small_pad(n), mp = small_pad(m);
   return static_cast<size_t>((np + mp) * (D + 2) + 2 * kSmallWarps * 32) * sizeof(float);
-}
-
-// Stores v at the address of `local` in the shared memory of CTA `rank` of the cluster and
-// counts its 4 bytes on that CTA's mbarrier at the address of `bar` (asynchronous store).
-__device__ __forceinline__ void st_async_cluster(float* local, unsigned rank, float v,
-                                                 uint64_t* bar) {
-  uint32_t ra, rb;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)),
-               "r"(rank));
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)),
-               "r"(rank));
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                   ra),
-               "r"(__float_as_uint(v)), "r"(rb)
-               : "memory");
-}
-
-// Bounded wait for a phase of an mbarrier that other CTAs of the cluster complete, with
-// acquire semantics at cluster scope (their stores are then visible here).
-__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_ns();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
-        : "memory");
-    if (done) return true;
-    if (global_ns() - t0 > kWaitLimitNs) return false;
-  }
 }
 
 // The bias of a point from its (float) potential and log2 weight, in double, rounded once.
