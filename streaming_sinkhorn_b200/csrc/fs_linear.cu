@@ -88,9 +88,17 @@ fs_status make_map(CUtensorMap* map, const void* data, int64_t rows, int64_t col
   return FS_OK;
 }
 
+// The two maps of a K-major A (its row blocks, and the last of them) and that block's rows.
+fs_status make_rows_maps(CUtensorMap* map, CUtensorMap* tail, uint32_t* tail_rows,
+                         const void* data, int64_t rows, int64_t cols, int64_t ld) {
+  *tail_rows = static_cast<uint32_t>(rows - (ceil_div(rows, kLinM) - 1) * kLinM);
+  const fs_status s = make_map(map, data, rows, cols, ld, kLinM);
+  return s != FS_OK ? s : make_map(tail, data, rows, cols, ld, static_cast<int>(*tail_rows));
+}
+
 template <int BN, bool A_MN, bool B_MN, int EPI>
-fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMap& b,
-                        const LinParams& P, int sms, cudaStream_t st) {
+fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMap& tail,
+                        const CUtensorMap& b, const LinParams& P, int sms, cudaStream_t st) {
   constexpr auto fn = linear_kernel<BN, A_MN, B_MN, EPI>;
   static PerDeviceOnce once;
   const fs_status s = once.run("cudaFuncSetAttribute", [&] {
@@ -100,7 +108,7 @@ fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMa
   if (s != FS_OK) return s;
   const int64_t grid = std::min<int64_t>(P.units, sms);
   return launch(what, fn, dim3(static_cast<unsigned>(grid)), kLinThreads, LinShape<BN>::SMEM, st,
-                1, a, b, P);
+                1, a, tail, b, P);
 }
 
 // The forward pass: tile width, column tiles of a unit, and how many units share a row block.
@@ -195,10 +203,17 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   const ForwardPlan p = forward_plan(x->rows, w->rows, sms);
   if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
   unsigned char* base = static_cast<unsigned char*>(ws);
-  CUtensorMap ma, mb;
-  if ((s = make_map(&ma, x->data, x->rows, x->cols, x->ld, kLinM)) != FS_OK) return s;
-  if ((s = make_map(&mb, w->data, w->rows, w->cols, w->ld, p.bn)) != FS_OK) return s;
+  unsigned* err = reinterpret_cast<unsigned*>(base);
+  float4* part = reinterpret_cast<float4*>(base + kHeader);
+  float* given = reinterpret_cast<float*>(base + p.off_given);
+  const float inv_eps = 1.0f / eps;
+  s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
+  if (s != FS_OK) return s;
+  CUtensorMap ma, mt, mb;
   LinParams P{};
+  s = make_rows_maps(&ma, &mt, &P.tail_rows, x->data, x->rows, x->cols, x->ld);
+  if (s != FS_OK) return s;
+  if ((s = make_map(&mb, w->data, w->rows, w->cols, w->ld, p.bn)) != FS_OK) return s;
   P.m = x->rows;
   P.n = w->rows;
   P.k_steps = static_cast<int32_t>(ceil_div(x->cols, kLinK));
@@ -207,31 +222,29 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   P.n_per_unit = static_cast<int32_t>(p.per_unit);
   P.k_splits = 1;
   P.units = p.m_blocks * p.splits;
-  P.err = reinterpret_cast<unsigned*>(base);
-  P.inv_eps = 1.0f / eps;
+  P.err = err;
+  P.inv_eps = inv_eps;
   P.ids = ids;
   P.ids_wide = ids_64;
-  P.part = reinterpret_cast<float4*>(base + kHeader);
-  P.given = reinterpret_cast<float*>(base + p.off_given);
+  P.part = part;
+  P.given = given;
   P.m_pad = p.m_pad;
   P.cols = w->rows;
-  s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
-  if (s != FS_OK) return s;
   s = p.bn == 128
-          ? launch_linear<128, false, false, kLinLse>("fs_linear_logprobs", ma, mb, P, sms, st)
-          : launch_linear<256, false, false, kLinLse>("fs_linear_logprobs", ma, mb, P, sms, st);
+          ? launch_linear<128, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st)
+          : launch_linear<256, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st);
   if (s != FS_OK) return s;
   LinJoinParams J{};
-  J.part = P.part;
-  J.given = P.given;
+  J.part = part;
+  J.given = given;
   J.parts = 2 * p.splits;
   J.m = x->rows;
   J.m_pad = p.m_pad;
   J.cols = w->rows;
   J.ids = ids;
   J.ids_wide = ids_64;
-  J.inv_eps = P.inv_eps;
-  J.err = P.err;
+  J.inv_eps = inv_eps;
+  J.err = err;
   J.logp = logp;
   J.entropy = entropy;
   J.lse = lse;
@@ -275,11 +288,12 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
   for (int64_t c = 0; c < p.chunks; ++c) {
     const int64_t col0 = c * p.chunk;
     const int64_t n = std::min(p.chunk, cols - col0);
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mt, mb;
     // G of the chunk: the scores again, and their gradient in the epilogue
-    if ((s = make_map(&ma, x->data, rows, dim, x->ld, kLinM)) != FS_OK) return s;
-    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256)) != FS_OK) return s;
     LinParams P{};
+    s = make_rows_maps(&ma, &mt, &P.tail_rows, x->data, rows, dim, x->ld);
+    if (s != FS_OK) return s;
+    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256)) != FS_OK) return s;
     P.m = rows;
     P.n = n;
     P.k_steps = static_cast<int32_t>(ceil_div(dim, kLinK));
@@ -301,12 +315,13 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     P.g_lse = g_lse;
     P.g_out = G;
     P.ld_g = p.ld_g;
-    s = launch_linear<256, false, false, kLinScoreGrad>("fs_linear_logprobs_grad (scores)", ma, mb,
-                                                        P, sms, st);
+    s = launch_linear<256, false, false, kLinScoreGrad>("fs_linear_logprobs_grad (scores)", ma, mt,
+                                                        mb, P, sms, st);
     if (s != FS_OK) return s;
     if (gx) {  // dx = G w: K runs along G's rows and down w's
       LinParams Q{};
-      if ((s = make_map(&ma, G, rows, n, p.ld_g, kLinM)) != FS_OK) return s;
+      s = make_rows_maps(&ma, &mt, &Q.tail_rows, G, rows, n, p.ld_g);
+      if (s != FS_OK) return s;
       if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 64)) != FS_OK) return s;
       Q.m = rows;
       Q.n = dim;
@@ -320,8 +335,8 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.acc = acc;
       Q.add = c > 0;
       Q.ld_out = dim;
-      s = launch_linear<256, false, true, kLinStore>("fs_linear_logprobs_grad (dx)", ma, mb, Q, sms,
-                                                     st);
+      s = launch_linear<256, false, true, kLinStore>("fs_linear_logprobs_grad (dx)", ma, mt, mb, Q,
+                                                     sms, st);
       if (s != FS_OK) return s;
     }
     if (gw) {  // dw = G^T x: K runs down both
@@ -339,8 +354,8 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.err = err;
       Q.out = gw + col0 * dim;
       Q.ld_out = dim;
-      s = launch_linear<256, true, true, kLinStore>("fs_linear_logprobs_grad (dw)", ma, mb, Q, sms,
-                                                    st);
+      s = launch_linear<256, true, true, kLinStore>("fs_linear_logprobs_grad (dw)", ma, ma, mb, Q,
+                                                    sms, st);
       if (s != FS_OK) return s;
     }
   }

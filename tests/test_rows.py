@@ -224,6 +224,19 @@ def test_linear_matches_float64(rows, cols, dim):
     check_linear(x, w, ids, seed=rows)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("dim,cols", [(256, 1000), (264, 77), (512, 20000), (1000, 333), (2048, 5003),
+                                      (4096, 1537), (4104, 300)])
+def test_linear_few_rows(rows, dim, cols):
+    x = rand(rows, dim, seed=rows, dtype=BF, scale=1.0)
+    w = rand(cols, dim + 8, seed=dim, dtype=BF, scale=2.0 / math.sqrt(dim))
+    ids = randint(rows, cols, seed=dim)
+    if rows > 2:
+        ids[1] = -1
+    for view in (w[:, :dim], w[:, :dim].contiguous()):
+        check_linear(x, view, ids, seed=rows)
+
+
 def test_linear_layouts_and_temperature():
     x, w = rand(40, 130, seed=1, dtype=BF, scale=1.0), rand(70, 130, seed=2, dtype=BF, scale=0.2)
     ids = randint(40, 70, dtype=torch.int32)
