@@ -96,24 +96,28 @@ fs_status make_rows_maps(CUtensorMap* map, CUtensorMap* tail, uint32_t* tail_row
   return s != FS_OK ? s : make_map(tail, data, rows, cols, ld, static_cast<int>(*tail_rows));
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
 fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMap& tail,
                         const CUtensorMap& b, const LinParams& P, int sms, cudaStream_t st) {
-  constexpr auto fn = linear_kernel<BN, A_MN, B_MN, EPI>;
+  constexpr auto fn = linear_kernel<BN, CG, A_MN, B_MN, EPI>;
   static PerDeviceOnce once;
   const fs_status s = once.run("cudaFuncSetAttribute", [&] {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(LinShape<BN>::SMEM));
+                                static_cast<int>(LinShape<BN, CG>::SMEM));
   });
   if (s != FS_OK) return s;
-  const int64_t grid = std::min<int64_t>(P.units, sms);
-  return launch(what, fn, dim3(static_cast<unsigned>(grid)), kLinThreads, LinShape<BN>::SMEM, st,
-                1, a, tail, b, P);
+  const int64_t grid = std::min<int64_t>(P.units, sms / CG) * CG;
+  return launch(what, fn, dim3(static_cast<unsigned>(grid)), kLinThreads, LinShape<BN, CG>::SMEM,
+                st, CG, a, tail, b, P);
 }
+
+// CTAs that share a tile of a product with this many rows: pairs once a pair has rows for both.
+int pair_of(int64_t rows) { return rows > kLinM ? 2 : 1; }
 
 // The forward pass: tile width, column tiles of a unit, and how many units share a row block.
 struct ForwardPlan {
   int bn;
+  int cg;  // CTAs of a tile
   int64_t m_blocks, n_blocks, per_unit, splits;
   int64_t m_pad;
   size_t off_given, total;
@@ -121,27 +125,29 @@ struct ForwardPlan {
 
 ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
   ForwardPlan p{};
-  p.m_blocks = ceil_div(rows, kLinM);
+  p.cg = pair_of(rows);
+  p.m_blocks = ceil_div(rows, kLinM * p.cg);
   // One row block reads w once and is bound by that read: narrow tiles spread it evenly over
   // the SMs. More row blocks are bound by the products: wide tiles.
-  p.bn = p.m_blocks == 1 ? 128 : 256;
+  p.bn = p.cg == 1 ? 128 : 256;
   p.n_blocks = ceil_div(cols, p.bn);
   // The split of the columns whose last wave is fullest; ties go to fewer parts.
   double best = 0.0;
   p.per_unit = 1;
   for (int64_t per = p.n_blocks; per >= 1; --per) {
     const int64_t units = p.m_blocks * ceil_div(p.n_blocks, per);
-    if (units > 16ll * sms && best > 0.0) break;
+    const int workers = sms / p.cg;
+    if (units > 16ll * workers && best > 0.0) break;
     // tiles the busiest CTA takes, against an even share
-    const double even = static_cast<double>(p.m_blocks * p.n_blocks) / sms;
-    const double eff = even / static_cast<double>(ceil_div(units, sms) * per);
+    const double even = static_cast<double>(p.m_blocks * p.n_blocks) / workers;
+    const double eff = even / static_cast<double>(ceil_div(units, workers) * per);
     if (eff > best + 1e-3) {
       best = eff;
       p.per_unit = per;
     }
   }
   p.splits = ceil_div(p.n_blocks, p.per_unit);
-  p.m_pad = p.m_blocks * kLinM;
+  p.m_pad = p.m_blocks * kLinM * p.cg;
   p.off_given = kHeader + static_cast<size_t>(2 * p.splits * p.m_pad) * sizeof(float4);
   p.total = round_up(p.off_given + static_cast<size_t>(p.m_pad) * 4, 256);
   return p;
@@ -162,13 +168,15 @@ BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
   p.ld_g = round_up(std::min(p.chunk, cols), 256);
   // dx has few tiles and a long K: split K so that the last wave is full, counting the write
   // and read of each split's fp32 partial sums (about 1 K step per 2^16 floats and SM)
-  const int64_t tiles = ceil_div(rows, kLinM) * ceil_div(dim, 256);
+  const int cg = pair_of(rows);
+  const int64_t tiles = ceil_div(rows, kLinM * cg) * ceil_div(dim, 256);
+  const int workers = sms / cg;
   const int64_t k_steps = ceil_div(std::min(p.chunk, cols), kLinK);
   double best = 0.0;
   p.splits = 1;
   for (int64_t s = 1; s <= 64 && s <= std::max<int64_t>(1, k_steps / 8); ++s) {
     const double product =
-        static_cast<double>(ceil_div(tiles * s, sms)) * static_cast<double>(ceil_div(k_steps, s));
+        static_cast<double>(ceil_div(tiles * s, workers)) * static_cast<double>(ceil_div(k_steps, s));
     const double sums = s > 1 ? static_cast<double>(s) * rows * dim * 8.0 / 6.0e12 / 2.8e-7 : 0.0;
     const double cost = product + sums;
     if (s == 1 || cost < best) {
@@ -213,7 +221,7 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   LinParams P{};
   s = make_rows_maps(&ma, &mt, &P.tail_rows, x->data, x->rows, x->cols, x->ld);
   if (s != FS_OK) return s;
-  if ((s = make_map(&mb, w->data, w->rows, w->cols, w->ld, p.bn)) != FS_OK) return s;
+  if ((s = make_map(&mb, w->data, w->rows, w->cols, w->ld, p.bn / p.cg)) != FS_OK) return s;
   P.m = x->rows;
   P.n = w->rows;
   P.k_steps = static_cast<int32_t>(ceil_div(x->cols, kLinK));
@@ -230,9 +238,10 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   P.given = given;
   P.m_pad = p.m_pad;
   P.cols = w->rows;
-  s = p.bn == 128
-          ? launch_linear<128, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st)
-          : launch_linear<256, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st);
+  P.last_block = static_cast<int32_t>(ceil_div(x->rows, kLinM) - 1);
+  s = p.cg == 1
+          ? launch_linear<128, 1, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st)
+          : launch_linear<256, 2, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st);
   if (s != FS_OK) return s;
   LinJoinParams J{};
   J.part = part;
@@ -285,6 +294,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
   s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
   if (s != FS_OK) return s;
   const __nv_bfloat16* wd = static_cast<const __nv_bfloat16*>(w->data);
+  const int cg = pair_of(rows);
   for (int64_t c = 0; c < p.chunks; ++c) {
     const int64_t col0 = c * p.chunk;
     const int64_t n = std::min(p.chunk, cols - col0);
@@ -293,11 +303,12 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     LinParams P{};
     s = make_rows_maps(&ma, &mt, &P.tail_rows, x->data, rows, dim, x->ld);
     if (s != FS_OK) return s;
-    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256)) != FS_OK) return s;
+    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256 / cg)) != FS_OK) return s;
     P.m = rows;
     P.n = n;
     P.k_steps = static_cast<int32_t>(ceil_div(dim, kLinK));
-    P.m_blocks = static_cast<int32_t>(ceil_div(rows, kLinM));
+    P.m_blocks = static_cast<int32_t>(ceil_div(rows, kLinM * cg));
+    P.last_block = static_cast<int32_t>(ceil_div(rows, kLinM) - 1);
     P.n_blocks = static_cast<int32_t>(ceil_div(n, 256));
     P.n_per_unit = 1;
     P.k_splits = 1;
@@ -315,8 +326,9 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     P.g_lse = g_lse;
     P.g_out = G;
     P.ld_g = p.ld_g;
-    s = launch_linear<256, false, false, kLinScoreGrad>("fs_linear_logprobs_grad (scores)", ma, mt,
-                                                        mb, P, sms, st);
+    const char* what = "fs_linear_logprobs_grad (scores)";
+    s = cg == 1 ? launch_linear<256, 1, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st)
+                : launch_linear<256, 2, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st);
     if (s != FS_OK) return s;
     if (gx) {  // dx = G w: K runs along G's rows and down w's
       LinParams Q{};
@@ -327,6 +339,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.n = dim;
       Q.k_steps = static_cast<int32_t>(ceil_div(n, kLinK));
       Q.m_blocks = P.m_blocks;
+      Q.last_block = P.last_block;
       Q.n_blocks = static_cast<int32_t>(ceil_div(dim, 256));
       Q.k_splits = static_cast<int32_t>(p.splits);
       Q.units = static_cast<int64_t>(Q.m_blocks) * Q.n_blocks * p.splits;
@@ -335,8 +348,9 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.acc = acc;
       Q.add = c > 0;
       Q.ld_out = dim;
-      s = launch_linear<256, false, true, kLinStore>("fs_linear_logprobs_grad (dx)", ma, mt, mb, Q,
-                                                     sms, st);
+      what = "fs_linear_logprobs_grad (dx)";
+      s = cg == 1 ? launch_linear<256, 1, false, true, kLinStore>(what, ma, mt, mb, Q, sms, st)
+                  : launch_linear<256, 2, false, true, kLinStore>(what, ma, mt, mb, Q, sms, st);
       if (s != FS_OK) return s;
     }
     if (gw) {  // dw = G^T x: K runs down both
@@ -346,7 +360,9 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.m = n;
       Q.n = dim;
       Q.k_steps = static_cast<int32_t>(ceil_div(rows, kLinK));
-      Q.m_blocks = static_cast<int32_t>(ceil_div(n, kLinM));
+      const int cw = pair_of(n);
+      Q.m_blocks = static_cast<int32_t>(ceil_div(n, kLinM * cw));
+      Q.last_block = static_cast<int32_t>(ceil_div(n, kLinM) - 1);
       Q.n_blocks = static_cast<int32_t>(ceil_div(dim, 256));
       Q.k_splits = 1;
       Q.n_fast = 1;  // the tiles of one strip of G run together
@@ -354,8 +370,9 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.err = err;
       Q.out = gw + col0 * dim;
       Q.ld_out = dim;
-      s = launch_linear<256, true, true, kLinStore>("fs_linear_logprobs_grad (dw)", ma, ma, mb, Q,
-                                                    sms, st);
+      what = "fs_linear_logprobs_grad (dw)";
+      s = cw == 1 ? launch_linear<256, 1, true, true, kLinStore>(what, ma, ma, mb, Q, sms, st)
+                  : launch_linear<256, 2, true, true, kLinStore>(what, ma, ma, mb, Q, sms, st);
       if (s != FS_OK) return s;
     }
   }

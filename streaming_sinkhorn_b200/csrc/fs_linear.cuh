@@ -13,7 +13,10 @@
 // One kernel does all four: C = A B^T over 64-wide K steps, warp 0 streams both operands
 // through a ring with TMA (128-byte swizzle), warp 1 issues the MMAs into one of two TMEM
 // accumulators, eight warps run the epilogue of the other (lane quarter warp % 4, half of the
-// columns each). An operand whose K runs along its rows' elements (x, w of the scores; G of
+// columns each). With more than 128 rows a pair of CTAs works on 256 x 256 tiles: each brings
+// its own 128 rows of A and half of B's 256, the first issues the MMAs of both, so B crosses
+// from L2 once for 256 rows. (A single CTA's 128 x 256 tile wants 96 bytes a clock of L2 at the
+// tensor cores' rate, a pair's 64 each.) An operand whose K runs along its rows' elements (x, w of the scores; G of
 // dx) is K-major; one whose K runs down its rows (w of dx; G and x of dw) is read as it lies as
 // an MN-major operand, so nothing is transposed in memory.
 //
@@ -40,10 +43,12 @@ constexpr uint32_t kLinRing = 192u * 1024u;           // bytes of the operand ri
 
 enum LinEpi : int { kLinLse = 0, kLinScoreGrad = 1, kLinStore = 2 };
 
-template <int BN>
+// CG: CTAs that share a tile (1 or 2).
+template <int BN, int CG>
 struct LinShape {
+  static constexpr int BOX_N = BN / CG;  // rows of B that a CTA brings
   static constexpr uint32_t A_BYTES = kLinM * kLinK * 2;
-  static constexpr uint32_t B_BYTES = BN * kLinK * 2;
+  static constexpr uint32_t B_BYTES = BOX_N * kLinK * 2;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = static_cast<int>(kLinRing / STAGE);
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
@@ -53,7 +58,8 @@ struct LinShape {
 struct LinParams {
   int64_t m, n;        // rows of C, columns of C that exist
   int32_t k_steps;     // of the whole product
-  int32_t m_blocks, n_blocks;
+  int32_t m_blocks, n_blocks;  // row blocks of a tile's height, column tiles
+  int32_t last_block;          // the last 128-row block of the matrix
   int32_t n_per_unit;  // column tiles of a unit (kLinLse)
   int32_t k_splits;    // parts of the K range (kLinStore)
   int32_t n_fast;      // units go along n first
@@ -99,13 +105,36 @@ __host__ __device__ constexpr uint32_t lin_idesc(int M, int N, bool a_mn, bool b
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// A box into this CTA's shared memory. With CG = 2 its bytes count on the barrier at this address
+// in the pair's first CTA (the address bit that tells the two apart cleared).
+template <int CG>
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
+  if constexpr (CG == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar) & 0xFEFFFFFFu)
+        : "memory");
+  }
+}
+
+// A commit that arrives in the issuing CTA alone.
+template <int CG>
+__device__ __forceinline__ void tc_commit_own(uint64_t* bar) {
+  if constexpr (CG == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
 }
 
 // What a unit covers: row block, column tiles [n0, n1), K steps [k0, k1), split.
@@ -142,12 +171,12 @@ __device__ __forceinline__ LinUnit lin_unit(const LinParams& P, int64_t u) {
   return r;
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <int BN, int CG, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_tail,
                   const __grid_constant__ CUtensorMap map_b, const LinParams P) {
-  using S = LinShape<BN>;
+  using S = LinShape<BN, CG>;
   extern __shared__ unsigned char lin_smem[];
   __shared__ uint64_t full_bar[S::STAGES], free_bar[S::STAGES];
   __shared__ uint64_t acc_bar[2], acc_free_bar[2];
@@ -157,6 +186,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   unsigned char* ring = lin_smem + ((1024u - (smem_u32(lin_smem) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = CG == 2 ? static_cast<int>(blockIdx.x & 1u) : 0;  // in the pair
+  const int64_t unit0 = blockIdx.x / CG, unit_step = gridDim.x / CG;
   volatile int* abort = &abort_sh;
 
   if (tid == 0) {
@@ -166,20 +197,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_bar[b], 1);
-      mbar_init(&acc_free_bar[b], kLinEpiWarps);
+      mbar_init(&acc_free_bar[b], CG * kLinEpiWarps);
     }
     mbar_init(&fin_bar, 1);
     abort_sh = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&tmem_base_sh)),
-                 "r"(S::TMEM));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_sh)),
+                   "r"(S::TMEM));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_sh)),
+                   "r"(S::TMEM));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_barrier();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
 
@@ -187,7 +226,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (lane == 0) {
       int64_t q = 0;
       bool ok = true;
-      for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+      for (int64_t u = unit0; ok && u < P.units; u += unit_step) {
         const LinUnit w = lin_unit<EPI>(P, u);
         for (int nb = w.n0; ok && nb < w.n1; ++nb) {
           for (int k = w.k0; k < w.k1; ++k, ++q) {
@@ -199,38 +238,48 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             unsigned char* a = ring + static_cast<uint32_t>(s) * S::STAGE;
             unsigned char* b = a + S::A_BYTES;
+            const int mb = w.mb * CG + rank;  // this CTA's 128 rows of A
+            if (rank == 0) {
+              // what all CTAs of the tile will bring (a block behind the last one: no rows)
+              uint32_t bytes = CG * S::B_BYTES;
+#pragma unroll
+              for (int c = 0; c < CG; ++c)
+                bytes += A_MN || mb + c < P.last_block ? S::A_BYTES
+                         : mb + c == P.last_block      ? P.tail_rows * 128u
+                                                       : 0u;
+              mbar_expect_tx(&full_bar[s], bytes);
+            }
             if constexpr (A_MN) {
-              mbar_expect_tx(&full_bar[s], S::STAGE);
 #pragma unroll
               for (int i = 0; i < kLinM / 64; ++i)
-                tma_load_2d(a + i * 8192, &map_a, w.mb * kLinM + i * 64, k * kLinK, &full_bar[s]);
-            } else {
-              const bool tail = w.mb == P.m_blocks - 1;
-              mbar_expect_tx(&full_bar[s], tail ? S::B_BYTES + P.tail_rows * 128u : S::STAGE);
-              tma_load_2d(a, tail ? &map_tail : &map_a, k * kLinK, w.mb * kLinM, &full_bar[s]);
+                tma_load_2d<CG>(a + i * 8192, &map_a, mb * kLinM + i * 64, k * kLinK, &full_bar[s]);
+            } else if (mb <= P.last_block) {
+              tma_load_2d<CG>(a, mb == P.last_block ? &map_tail : &map_a, k * kLinK, mb * kLinM,
+                              &full_bar[s]);
             }
             if constexpr (B_MN) {
 #pragma unroll
-              for (int i = 0; i < BN / 64; ++i)
-                tma_load_2d(b + i * 8192, &map_b, nb * BN + i * 64, k * kLinK, &full_bar[s]);
+              for (int i = 0; i < S::BOX_N / 64; ++i)
+                tma_load_2d<CG>(b + i * 8192, &map_b, nb * BN + rank * S::BOX_N + i * 64, k * kLinK,
+                                &full_bar[s]);
             } else {
-              tma_load_2d(b, &map_b, k * kLinK, nb * BN, &full_bar[s]);
+              tma_load_2d<CG>(b, &map_b, k * kLinK, nb * BN + rank * S::BOX_N, &full_bar[s]);
             }
           }
         }
       }
-      if (*abort)  // the copies in flight land before the CTA's shared memory goes
+      if (*abort && rank == 0)  // the copies in flight land before the shared memory goes
         for (int64_t v = q > S::STAGES ? q - S::STAGES : 0; v < q; ++v)
           (void)mbar_wait_bounded(&full_bar[v % S::STAGES],
                                   static_cast<uint32_t>(v / S::STAGES) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = lin_idesc(kLinM, BN, A_MN, B_MN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = lin_idesc(CG * kLinM, BN, A_MN, B_MN);
       int64_t q = 0;
       uint32_t t = 0;
       bool ok = true;
-      for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+      for (int64_t u = unit0; ok && u < P.units; u += unit_step) {
         const LinUnit w = lin_unit<EPI>(P, u);
         for (int nb = w.n0; ok && nb < w.n1; ++nb, ++t) {
           const uint32_t b = t & 1u;
@@ -253,15 +302,26 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               // 16 elements of K: 32 bytes along a K-major row, 16 rows of an MN-major box
               const uint64_t da = lin_desc(a0 + i * (A_MN ? 2048u : 32u), A_MN ? 8192u : 16u);
               const uint64_t db = lin_desc(b0 + i * (B_MN ? 2048u : 32u), B_MN ? 8192u : 16u);
-              tc_mma_f16(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
+              if constexpr (CG == 1)
+                tc_mma_f16(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
+              else
+                tc_mma_f16_pair(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
             }
-            tc_commit(&free_bar[s]);
+            if constexpr (CG == 1)
+              tc_commit(&free_bar[s]);
+            else
+              tc_commit_pair(&free_bar[s]);
           }
-          if (ok) tc_commit(&acc_bar[b]);
+          if (ok) {
+            if constexpr (CG == 1)
+              tc_commit(&acc_bar[b]);
+            else
+              tc_commit_pair(&acc_bar[b]);
+          }
         }
       }
       // every MMA issued has completed once fin_bar fires: TMEM is never released under one
-      tc_commit(&fin_bar);
+      tc_commit_own<CG>(&fin_bar);
       (void)mbar_wait_bounded(&fin_bar, 0);
     }
   } else if (warp >= 4) {
@@ -271,9 +331,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const float k2 = P.inv_eps * kLog2e;
     uint32_t t = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < P.units; u += gridDim.x) {
+    for (int64_t u = unit0; ok && u < P.units; u += unit_step) {
       const LinUnit w = lin_unit<EPI>(P, u);
-      const int64_t row = static_cast<int64_t>(w.mb) * kLinM + r;
+      const int64_t row = (static_cast<int64_t>(w.mb) * CG + rank) * kLinM + r;
       const bool live = row < P.m;
       // per row of the unit
       TokenSum sum = {-INFINITY, 0.0f, 0.0f};
@@ -385,7 +445,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_free_bar[b]);
+        if (lane == 0) {
+          if constexpr (CG == 1)
+            mbar_arrive(&acc_free_bar[b]);
+          else
+            mbar_arrive_cluster(&acc_free_bar[b], 0);  // the first CTA issues for both
+        }
       }
       if (EPI == kLinLse && ok)
         P.part[(static_cast<int64_t>(w.split) * 2 + grp) * P.m_pad + row] =
@@ -395,11 +460,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // neither CTA of a pair leaves while the other's MMAs, copies or arrivals may reach it
+  if constexpr (CG == 2) cluster_barrier();
   tc_fence_after();
   if (abort_sh && tid == 0) atomicOr(P.err, kErrTimeout);
-  if (warp == 2)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(S::TMEM));
+  if (warp == 2) {
+    if constexpr (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(S::TMEM));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(S::TMEM));
+  }
 }
 
 // ---- joining the parts -------------------------------------------------------------------------

@@ -29,6 +29,26 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
       : "memory");
 }
 
+// The same for a pair of CTAs (a cluster of two): issued by the pair's first CTA for both, each
+// CTA's tensor memory taking half of the rows; the commit arrives on the barrier at this address
+// in both.
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 // 32 consecutive fp32 columns of this thread's TMEM lane; the caller waits (tcgen05.wait::ld).
 __device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -79,6 +99,13 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
       }
     }
   }
+}
+
+// An arrival on the barrier at this address in CTA `rank` of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
