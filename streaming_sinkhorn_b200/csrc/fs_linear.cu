@@ -236,7 +236,7 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   P.ids_wide = ids_64;
   P.part = part;
   P.given = given;
-  P.m_pad = p.m_pad;
+  P.parts = 2 * p.splits;
   P.cols = w->rows;
   P.last_block = static_cast<int32_t>(ceil_div(x->rows, kLinM) - 1);
   s = p.cg == 1
@@ -246,9 +246,8 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   LinJoinParams J{};
   J.part = part;
   J.given = given;
-  J.parts = 2 * p.splits;
+  J.parts = P.parts;
   J.m = x->rows;
-  J.m_pad = p.m_pad;
   J.cols = w->rows;
   J.ids = ids;
   J.ids_wide = ids_64;

