@@ -50,7 +50,11 @@ struct LinShape {
   static constexpr int BOX_N = BN / CG;  // rows of B that a CTA brings
   static constexpr uint32_t A_BYTES = kLinM * kLinK * 2;
   static constexpr uint32_t B_BYTES = BOX_N * kLinK * 2;
-  static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+  // K steps of a stage. A lone row block is bound by the read of B: 256 neighbouring bytes of each
+  // row asked for together come faster than 128.
+  static constexpr int KS = CG == 1 && BN == 128 ? 2 : 1;
+  static constexpr uint32_t STEP = A_BYTES + B_BYTES;
+  static constexpr uint32_t STAGE = KS * STEP;
   static constexpr int STAGES = static_cast<int>(kLinRing / STAGE);
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
   static constexpr uint32_t TMEM = 2 * BN;  // two accumulators
@@ -230,15 +234,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int64_t u = unit0; ok && u < P.units; u += unit_step) {
         const LinUnit w = lin_unit<EPI>(P, u);
         for (int nb = w.n0; ok && nb < w.n1; ++nb) {
-          for (int k = w.k0; k < w.k1; ++k, ++q) {
+          for (int k = w.k0; k < w.k1; k += S::KS, ++q) {
             const int s = static_cast<int>(q % S::STAGES);
             const uint32_t round = static_cast<uint32_t>(q / S::STAGES);
             if (round > 0 && !tc_wait(&free_bar[s], (round - 1) & 1u, abort)) {
               ok = false;
               break;
             }
-            unsigned char* a = ring + static_cast<uint32_t>(s) * S::STAGE;
-            unsigned char* b = a + S::A_BYTES;
+            unsigned char* stage = ring + static_cast<uint32_t>(s) * S::STAGE;
             const int mb = w.mb * CG + rank;  // this CTA's 128 rows of A
             if (rank == 0) {
               // what all CTAs of the tile will bring (a block behind the last one: no rows)
@@ -248,23 +251,34 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 bytes += A_MN || mb + c < P.last_block ? S::A_BYTES
                          : mb + c == P.last_block      ? P.tail_rows * 128u
                                                        : 0u;
-              mbar_expect_tx(&full_bar[s], bytes);
+              mbar_expect_tx(&full_bar[s], S::KS * bytes);
             }
-            if constexpr (A_MN) {
+            // (a stage's steps behind the last one read as zero)
 #pragma unroll
-              for (int i = 0; i < kLinM / 64; ++i)
-                tma_load_2d<CG>(a + i * 8192, &map_a, mb * kLinM + i * 64, k * kLinK, &full_bar[s]);
-            } else if (mb <= P.last_block) {
-              tma_load_2d<CG>(a, mb == P.last_block ? &map_tail : &map_a, k * kLinK, mb * kLinM,
-                              &full_bar[s]);
+            for (int j = 0; j < S::KS; ++j) {
+              const int x = (k + j) * kLinK;
+              unsigned char* b = stage + j * S::STEP + S::A_BYTES;
+              if constexpr (B_MN) {
+#pragma unroll
+                for (int i = 0; i < S::BOX_N / 64; ++i)
+                  tma_load_2d<CG>(b + i * 8192, &map_b, nb * BN + rank * S::BOX_N + i * 64, x,
+                                  &full_bar[s]);
+              } else {
+                tma_load_2d<CG>(b, &map_b, x, nb * BN + rank * S::BOX_N, &full_bar[s]);
+              }
             }
-            if constexpr (B_MN) {
 #pragma unroll
-              for (int i = 0; i < S::BOX_N / 64; ++i)
-                tma_load_2d<CG>(b + i * 8192, &map_b, nb * BN + rank * S::BOX_N + i * 64, k * kLinK,
+            for (int j = 0; j < S::KS; ++j) {
+              const int x = (k + j) * kLinK;
+              unsigned char* a = stage + j * S::STEP;
+              if constexpr (A_MN) {
+#pragma unroll
+                for (int i = 0; i < kLinM / 64; ++i)
+                  tma_load_2d<CG>(a + i * 8192, &map_a, mb * kLinM + i * 64, x, &full_bar[s]);
+              } else if (mb <= P.last_block) {
+                tma_load_2d<CG>(a, mb == P.last_block ? &map_tail : &map_a, x, mb * kLinM,
                                 &full_bar[s]);
-            } else {
-              tma_load_2d<CG>(b, &map_b, k * kLinK, nb * BN + rank * S::BOX_N, &full_bar[s]);
+              }
             }
           }
         }
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             break;
           }
           tc_fence_after();
-          for (int k = w.k0; k < w.k1; ++k, ++q) {
+          for (int k = w.k0; k < w.k1; k += S::KS, ++q) {
             const int s = static_cast<int>(q % S::STAGES);
             if (!tc_wait(&full_bar[s], static_cast<uint32_t>(q / S::STAGES) & 1u, abort)) {
               ok = false;
@@ -299,14 +313,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const uint32_t a0 = smem_u32(ring + static_cast<uint32_t>(s) * S::STAGE);
             const uint32_t b0 = a0 + S::A_BYTES;
 #pragma unroll
-            for (int i = 0; i < kLinK / 16; ++i) {
+            for (int ji = 0; ji < S::KS * kLinK / 16; ++ji) {
+              const int i = ji % (kLinK / 16);
+              const uint32_t o = ji / (kLinK / 16) * S::STEP;
               // 16 elements of K: 32 bytes along a K-major row, 16 rows of an MN-major box
-              const uint64_t da = lin_desc(a0 + i * (A_MN ? 2048u : 32u), A_MN ? 8192u : 16u);
-              const uint64_t db = lin_desc(b0 + i * (B_MN ? 2048u : 32u), B_MN ? 8192u : 16u);
+              const uint64_t da = lin_desc(a0 + o + i * (A_MN ? 2048u : 32u), A_MN ? 8192u : 16u);
+              const uint64_t db = lin_desc(b0 + o + i * (B_MN ? 2048u : 32u), B_MN ? 8192u : 16u);
               if constexpr (CG == 1)
-                tc_mma_f16(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
+                tc_mma_f16(tmem + b * BN, da, db, idesc, (k > w.k0 || ji > 0) ? 1u : 0u);
               else
-                tc_mma_f16_pair(tmem + b * BN, da, db, idesc, (k > w.k0 || i > 0) ? 1u : 0u);
+                tc_mma_f16_pair(tmem + b * BN, da, db, idesc, (k > w.k0 || ji > 0) ? 1u : 0u);
             }
             if constexpr (CG == 1)
               tc_commit(&free_bar[s]);
