@@ -519,10 +519,10 @@ FS_API fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt,
  * Sinkhorn potentials of a given score matrix: the alternating updates of fs_potentials for
  * C = -s, s = softmax(z) or sigmoid(z) by row, uniform row weights and column weights
  * proportional to load (experts, >= 0; NULL for uniform; it is normalised):
- *   g <- g_init (or 0);  repeat n_iters times:
+ *   g <- g_init (or 0);  repeat n_iters (1 .. 10^6) times:
  *     f_i <- -eps log sum_j b_j e^((s_ij + g_j)/eps),   b_j = load_j / sum load
  *     g_j <- -eps log mean_i e^((s_ij + f_i)/eps)
- * f (rows), g (experts), float32. The plan b_j e^((s_ij + f_i + g_j)/eps) / rows has the load's
+ * f (rows), g (experts; may alias g_init), float32. The plan b_j e^((s_ij + f_i + g_j)/eps) / rows has the load's
  * column sums, and its largest entry in a row is where s_ij + g_j + eps log b_j is: with that
  * bias (g alone for a uniform load) fs_route's first pick follows the load as far as the plan
  * is sharp (small eps); for k > 1 the further picks are evened out only roughly.

@@ -3,6 +3,8 @@
 #pragma once
 
 #include <atomic>
+#include <cmath>
+#include <cstdint>
 #include <cuda_runtime.h>
 
 #include "../../include/fs.h"
@@ -103,6 +105,11 @@ fs_status launch(const char* what, void (*kernel)(P...), dim3 grid, int threads,
   const fs_status s = cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...), what);
   if (s == FS_OK) count_launches(1);
   return s;
+}
+
+// A temperature: its inverse, in base 2 too, is a factor of float32 arithmetic.
+inline fs_status check_eps(float eps) {
+  return std::isfinite(eps) && eps > 0.0f && std::isfinite(1.5f / eps) ? FS_OK : FS_ERR_EPS;
 }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

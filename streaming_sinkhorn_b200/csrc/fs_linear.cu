@@ -37,7 +37,7 @@ fs_status check_pair(const fs_matrix* x, const fs_matrix* w, float eps) {
   if (s != FS_OK) return s;
   if ((s = check_operand(w)) != FS_OK) return s;
   if (x->cols != w->cols || w->rows < 1) return FS_ERR_SHAPE;
-  return std::isfinite(eps) && eps > 0.0f && std::isfinite(1.0f / eps) ? FS_OK : FS_ERR_EPS;
+  return check_eps(eps);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -131,20 +131,23 @@ ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
   // the SMs. More row blocks are bound by the products: wide tiles.
   p.bn = p.cg == 1 ? 128 : 256;
   p.n_blocks = ceil_div(cols, p.bn);
-  // The split of the columns whose last wave is fullest; ties go to fewer parts.
+  // The split of the columns whose last wave is fullest, of those that fill 1 .. 16 waves; ties go
+  // to fewer parts.
+  const int workers = sms / p.cg;
+  const double even = static_cast<double>(p.m_blocks * p.n_blocks) / workers;
   double best = 0.0;
-  p.per_unit = 1;
-  for (int64_t per = p.n_blocks; per >= 1; --per) {
+  p.per_unit = p.n_blocks;
+  for (int64_t wave = 1; wave <= 16; ++wave) {
+    const int64_t splits = std::max<int64_t>(1, workers * wave / p.m_blocks);
+    const int64_t per = ceil_div(p.n_blocks, std::min(splits, p.n_blocks));
     const int64_t units = p.m_blocks * ceil_div(p.n_blocks, per);
-    const int workers = sms / p.cg;
-    if (units > 16ll * workers && best > 0.0) break;
-    // tiles the busiest CTA takes, against an even share
-    const double even = static_cast<double>(p.m_blocks * p.n_blocks) / workers;
+    // an even share, against the tiles that the busiest worker takes
     const double eff = even / static_cast<double>(ceil_div(units, workers) * per);
     if (eff > best + 1e-3) {
       best = eff;
       p.per_unit = per;
     }
+    if (per == 1) break;
   }
   p.splits = ceil_div(p.n_blocks, p.per_unit);
   p.m_pad = p.m_blocks * kLinM * p.cg;

@@ -13,6 +13,7 @@ namespace fs {
 namespace {
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int32_t kMaxIters = 1000000;  // two arrivals a CTA and iteration stay below 2^32
 
 fs_status check_matrix(const fs_matrix* z) {
   if (!z) return FS_ERR_NULL;
@@ -23,11 +24,6 @@ fs_status check_matrix(const fs_matrix* z) {
   if (z->rows > 0 && !z->data) return FS_ERR_NULL;
   if (!aligned(z->data, z->dtype == FS_F32 ? 4 : 2)) return FS_ERR_ALIGNMENT;
   return FS_OK;
-}
-
-fs_status check_eps(float eps) {
-  // 1 / eps is used as a factor
-  return std::isfinite(eps) && eps > 0.0f && std::isfinite(1.0f / eps) ? FS_OK : FS_ERR_EPS;
 }
 
 // Calls f with a null pointer of the matrix's element type.
@@ -412,7 +408,7 @@ fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
   if (s != FS_OK) return s;
   if ((s = check_eps(eps)) != FS_OK) return s;
   if (score != FS_SCORE_SOFTMAX && score != FS_SCORE_SIGMOID) return FS_ERR_OPTION;
-  if (n_iters < 1) return FS_ERR_ITERS;
+  if (n_iters < 1 || n_iters > kMaxIters) return FS_ERR_ITERS;
   if (z->rows == 0) return FS_OK;
   if (!f || !g) return FS_ERR_NULL;
   if (!aligned(load, 4) || !aligned(g_init, 4) || !aligned(f, 4) || !aligned(g, 4))

@@ -1,12 +1,14 @@
 """Log probabilities of given tokens, routing and balancing (GPU) against float64 references at
 the sizes, layouts and masks where they can go wrong, and their gradients against the formula
 and against differences. The references and tolerances are in rows_util."""
+import ctypes
 import math
 
 import pytest
 import torch
 
 import streaming_sinkhorn_b200 as fs
+from streaming_sinkhorn_b200 import _lib, rows
 from tests import rows_util as ru
 
 pytestmark = pytest.mark.gpu
@@ -89,6 +91,26 @@ def test_gradient_of_a_broadcast_row_is_the_sum():
     (g,) = torch.autograd.grad(out.logprobs.sum(), one)
     ref = ru.token_ref(one.expand(5, 303), ids, g_logp=torch.ones(5))["grad"].sum(0, keepdim=True)
     ru.assert_near(g, ref, 5 * 64 * ru.U, "summed gradient")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_tokens_alternatives_of_unkind_rows(dtype):
+    """Rows that defeat a bar taken from their beginning: ascending, all equal, a few values only,
+    the best at the ends, and long rows with more of them than a warp sets aside at once."""
+    v = 30000
+    z = rand(7, v, seed=21, dtype=dtype)
+    z[0] = torch.linspace(-4, 4, v).to(dtype)
+    z[1] = -torch.linspace(-4, 4, v).to(dtype)
+    z[2] = 1.5
+    z[3] = torch.randint(0, 3, (v,), generator=torch.Generator().manual_seed(1)).to(dtype)
+    z[4, 0], z[4, v - 1], z[4, v - 2] = 50.0, 49.0, 50.0
+    z[5, ::3] = 9.0
+    for top in (1, 20, 32):
+        check_tokens(z, randint(7, v), top=top, grads=False)
+        check_tokens(z[:, 1:-2], randint(7, v - 3), top=top, grads=False)
+    many = rand(700, 5000, seed=22, dtype=dtype)
+    many[::5] = 0.25
+    check_tokens(many, randint(700, 5000), top=32, grads=False)
 
 
 def test_tokens_ties_take_the_lowest_index():
@@ -530,6 +552,42 @@ def test_other_streams_and_two_calls_at_once():
         for x, y in zip(want, g):
             for t, u in zip(x, y):
                 assert (t is None and u is None) or torch.equal(t, u)
+
+
+def test_balance_over_the_whole_grid_at_once_and_captured():
+    """Two calls that each want every SM, on two streams, and one in a graph."""
+    z = rand(60000, 250, seed=79, scale=1.0)
+    want = fs.balance(z, score="sigmoid", eps=0.1, n_iters=5)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(fs.balance(z, score="sigmoid", eps=0.1, n_iters=5))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fs.balance(z, score="sigmoid", eps=0.1, n_iters=5)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for f, g in (*got, out):
+        assert torch.equal(f, want[0]) and torch.equal(g, want[1])
+
+
+def test_balance_many_iterations_and_g_in_place():
+    z = rand(900, 40, seed=80, scale=1.0)
+    check_balance(z, 0.1, 200, "sigmoid")
+    g0 = rand(40, seed=85, scale=0.1)
+    f, g = check_balance(z, 0.1, 3, g_init=g0)
+    lib, m = _lib.load(), rows._matrix(z)
+    ws = torch.empty(lib.fs_balance_workspace_bytes(ctypes.byref(m)), dtype=torch.uint8, device="cuda")
+    f2 = torch.empty_like(f)
+    code = lib.fs_balance(ctypes.byref(m), 0, 0.1, 3, None, g0.data_ptr(), f2.data_ptr(),
+                          g0.data_ptr(), ws.data_ptr(), ws.numel(),
+                          torch.cuda.current_stream().cuda_stream)
+    assert code == 0 and torch.equal(f, f2) and torch.equal(g, g0)
 
 
 def test_captured_into_a_graph_and_replayed():

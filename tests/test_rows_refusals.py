@@ -83,7 +83,7 @@ def test_bad_matrices(z, expect):
 
 
 def test_token_arguments():
-    for eps in (0.0, -1.0, NAN, INF, 1e-45):
+    for eps in (0.0, -1.0, NAN, INF, 1e-45, 3e-39):
         assert tokens(eps=eps) == "FS_ERR_EPS" and tokens_grad(eps=eps) == "FS_ERR_EPS"
     for top in (-1, 33):
         assert tokens(top=top) == "FS_ERR_OPTION" and tokens_grad(top=top) == "FS_ERR_OPTION"
@@ -131,7 +131,7 @@ def test_balance_arguments():
     assert big > (1 << 20) * 256 * 4 * 3 // 4
     assert balance(mat(cols=1025)) == "FS_ERR_SHAPE"
     assert balance(eps=0.0) == "FS_ERR_EPS" and balance(eps=NAN) == "FS_ERR_EPS"
-    assert balance(n_iters=0) == "FS_ERR_ITERS"
+    assert balance(n_iters=0) == "FS_ERR_ITERS" and balance(n_iters=1000001) == "FS_ERR_ITERS"
     assert balance(score=2) == "FS_ERR_OPTION"
     assert balance(f=None) == "FS_ERR_NULL" and balance(g=None) == "FS_ERR_NULL"
     assert balance(load=FAKE + 2) == "FS_ERR_ALIGNMENT"
