@@ -187,11 +187,11 @@ __device__ __forceinline__ float4 bal_load(const T* z, int j, int E, bool vec) {
                      j + 3 < E ? Elem<T>::to_f(z[j + 3]) : -INFINITY);
 }
 
-// log2 of a positive float in two parts, so that a large offset meets the whole number first.
-__device__ __forceinline__ float bal_log2(float v, float offset) {
+// log2 of a positive float about two offsets, the whole numbers added up in 64 bits.
+__device__ __forceinline__ double bal_log2(float v, float off, float extra) {
   int k;
   const float f = frexpf(v, &k);
-  return (offset + static_cast<float>(k)) + log2f(f);
+  return (static_cast<double>(off) + extra + k) + log2f(f);
 }
 
 template <typename T, int NL, int LPT, int NW, bool CLUSTER>
@@ -202,20 +202,22 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
   constexpr int kParts = kQuads >= S::kThreads ? 1 : (S::kThreads / kQuads < NW
                                                           ? S::kThreads / kQuads
                                                           : NW);
-  extern __shared__ __align__(16) float bal_smem[];
+  extern __shared__ __align__(16) double bal_smem[];
   __shared__ int ok_sh;
   __shared__ float warp_sh[2][NW];
   __shared__ uint64_t part_bar[2];  // CLUSTER: all CTAs' sums have arrived (by parity)
   __shared__ int redo_sh;
-  float* gam = bal_smem;              // [cols] gamma
-  float* lb = gam + S::kCols;         // [cols] log2 beta
+  // gamma is carried in 64 bits: it is a sum over the iterations, and next to 20 (eps = 0.05) a
+  // float's rounding would show in g
+  double* gam = bal_smem;                                  // [cols]
+  float* lb = reinterpret_cast<float*>(gam + S::kCols);    // [cols] log2 beta
   float* csum = lb + S::kCols;        // [NW][cols] partial sums
   float* parts = csum + NW * S::kCols;  // CLUSTER: [2][16][kPartCols]
   float* u_res = parts + (CLUSTER ? 2 * kBalMaxCluster * kPartCols : 0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int l = lane % LPT, grp = lane / LPT;
   const int E = P.experts;
-  const float ke = kLog2e / P.eps;
+  const float ke = kLog2e / P.eps, inv_e = 1.0f / static_cast<float>(E);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * P.per_cta;
   const int n = static_cast<int>(
       P.rows - row0 < P.per_cta ? (P.rows > row0 ? P.rows - row0 : 0) : P.per_cta);
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
       else if (P.load)
         b = static_cast<float>(log2(static_cast<double>(P.load[j]) * E / tot));
       lb[j] = b;
-      gam[j] = j < E ? (P.g_init ? P.g_init[j] * ke : 0.0f) + b : -INFINITY;
+      gam[j] = j < E ? (P.g_init ? static_cast<double>(P.g_init[j]) * ke : 0.0) + b : -INFINITY;
     }
   }
 
@@ -331,14 +333,14 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     float off = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      gm[i] = gam[S::column(l, i)];
+      gm[i] = static_cast<float>(gam[S::column(l, i)]);
       off = fmaxf(off, gm[i]);
       acc[i] = 0.0f;
     }
     off = group_max<LPT>(off);
     off = (off == -INFINITY ? 0.0f : off) + umax;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) gm[i] -= off;
+    for (int i = 0; i < NL; ++i) gm[i] = static_cast<float>(gam[S::column(l, i)] - off);
     // Rows are read one step ahead; with 16 warps two rows a step (b + grp and the next
     // group's). More than 256 columns leave no registers for either.
     constexpr int kH = NL == 8 && NW == 16 ? 2 : 1;
@@ -380,7 +382,11 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
         const int r = b + h * S::kGroups + grp;
-        const float w = sum[h] == 0.0f ? 0.0f : __fdividef(static_cast<float>(E), sum[h]);
+        // One correction of the quick quotient: its error has a sign, and one that all rows share
+        // would move every gamma the same way in every iteration.
+        float w = sum[h] == 0.0f ? 0.0f : __fdividef(static_cast<float>(E), sum[h]);
+        w = fmaf(w * inv_e, fmaf(-w, sum[h], static_cast<float>(E)), w);
+        if (sum[h] == 0.0f) w = 0.0f;
         const u64 w2 = pk(w, w);
 #pragma unroll
         for (int i = 0; i < NL; i += 2) {
@@ -388,9 +394,9 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
           upk(a, acc[i], acc[i + 1]);
         }
         if (last && r < n && l == 0)
-          P.f[row0 + r] =
-              sum[h] == 0.0f ? 0.0f
-                             : -bal_log2(sum[h] / static_cast<float>(E), off + extra[h]) / ke;
+          P.f[row0 + r] = sum[h] == 0.0f
+                              ? 0.0f
+                              : static_cast<float>(-bal_log2(sum[h] * inv_e, off, extra[h]) / ke);
       }
     }
     // the CTA's column sums: rows of a warp, then the warps in their order
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
         redo_sh = 1;
       } else {
         // the gamma that the rows have seen is the rounded one less the offset
-        gam[j] = ((gam[j] - off) + off) - log2f(c) + lb[j];
+        gam[j] = (static_cast<double>(static_cast<float>(gam[j] - off)) + off) - log2f(c) + lb[j];
       }
     }
     __syncthreads();
@@ -500,14 +506,16 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
           float m = -INFINITY;
           for (int k = 0; k < E; ++k) {
             const float ck = csum[k];
-            const float gk = lb[k] == -INFINITY || ck < kBalFlushed ? gam[k] : gam[k] + log2f(ck) - lb[k];
+            const float gk = static_cast<float>(
+                lb[k] == -INFINITY || ck < kBalFlushed ? gam[k] : gam[k] + log2f(ck) - lb[k]);
             m = fmaxf(m, src[k] + gk);
           }
           if (m == -INFINITY) continue;
           float sum = 0.0f;
           for (int k = 0; k < E; ++k) {
             const float ck = csum[k];
-            const float gk = lb[k] == -INFINITY || ck < kBalFlushed ? gam[k] : gam[k] + log2f(ck) - lb[k];
+            const float gk = static_cast<float>(
+                lb[k] == -INFINITY || ck < kBalFlushed ? gam[k] : gam[k] + log2f(ck) - lb[k]);
             sum += ex2(src[k] + gk - m);
           }
           const float x = src[j] - (m + log2f(sum / static_cast<float>(E)));
@@ -555,7 +563,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
   }
   if (blockIdx.x == 0)
     for (int j = tid; j < E; j += S::kThreads)
-      P.g[j] = lb[j] == -INFINITY ? -INFINITY : (gam[j] - lb[j]) / ke;
+      P.g[j] = lb[j] == -INFINITY ? -INFINITY : static_cast<float>((gam[j] - lb[j]) / ke);
 }
 
 }  // namespace fs

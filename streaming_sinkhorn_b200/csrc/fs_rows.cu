@@ -295,7 +295,7 @@ BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   while (p.nl * p.lpt < experts) p.lpt *= 2;
   p.cols = p.nl * p.lpt;
   const size_t cluster_fixed =
-      static_cast<size_t>(2 + kBalClusterWarps) * p.cols * 4 + 2ull * kBalMaxCluster * (p.cols + 4) * 4;
+      static_cast<size_t>(3 + kBalClusterWarps) * p.cols * 4 + 2ull * kBalMaxCluster * (p.cols + 4) * 4;
   const size_t row = static_cast<size_t>(p.cols) * 4;
   const int64_t step = (32 / p.lpt) * kBalClusterWarps;  // rows a CTA takes at once
   auto spread = [&](int64_t ctas) {
@@ -322,7 +322,7 @@ BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   // The grid's CTAs have many rows each and hide their latencies with more warps, where the
   // registers allow it.
   p.nw = p.cluster || p.nl > 8 ? kBalClusterWarps : kBalGridWarps;
-  const size_t used = p.cluster ? cluster_fixed : static_cast<size_t>(2 + p.nw) * p.cols * 4;
+  const size_t used = p.cluster ? cluster_fixed : static_cast<size_t>(3 + p.nw) * p.cols * 4;
   p.resident = static_cast<int>(std::min<int64_t>(p.per_cta, (kBalSmemBudget - used) / row));
   p.smem = used + p.resident * row;
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
