@@ -86,6 +86,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned* sync, unsigned target, in
 template <int NL, int LPT, int NW>
 struct BalShape {
   static constexpr int kThreads = NW * 32;
+  static constexpr int kQuads = NL * LPT / 4;
   static constexpr int kCols = NL * LPT;
   static constexpr int kGroups = 32 / LPT;               // rows a warp takes at once
   static constexpr int kRowStep = kGroups * NW;          // rows a CTA takes at once
@@ -137,7 +138,8 @@ __device__ __forceinline__ void bal_rows(const float4 (*u)[NL / 4], const float*
   for (int h = 0; h < H; ++h) sum[h] = group_sum<LPT>(sum[h]);
   bool any = sum[0] < kBalLowSum;
   if (H == 2) any |= sum[H - 1] < kBalLowSum;
-  if (__any_sync(0xffffffffu, any)) {
+  if (LPT < 32) any = __any_sync(0xffffffffu, any);  // (whole warps have one row: one sum)
+  if (any) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       float m = -INFINITY;
@@ -198,7 +200,7 @@ template <typename T, int NL, int LPT, int NW, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams P) {
   using S = BalShape<NL, LPT, NW>;
   constexpr int kPartCols = S::kCols + 4;  // column sums, then the open rows
-  constexpr int kQuads = S::kCols / 4;
+  constexpr int kQuads = S::kQuads;
   constexpr int kParts = kQuads >= S::kThreads ? 1 : (S::kThreads / kQuads < NW
                                                           ? S::kThreads / kQuads
                                                           : NW);
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     cluster_barrier();  // no CTA writes into another's shared memory before that one is ready
   }
 
-  float open_rows = 0.0f;
+  double inv_open = 0.0;  // 1 / rows that take part
   bool alive = true;
   for (int it = 0; it < P.n_iters && alive; ++it) {
     const bool last = it == P.n_iters - 1;
@@ -341,50 +343,20 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     off = (off == -INFINITY ? 0.0f : off) + umax;
 #pragma unroll
     for (int i = 0; i < NL; ++i) gm[i] = static_cast<float>(gam[S::column(l, i)] - off);
-    // Rows are read one step ahead; with 16 warps two rows a step (b + grp and the next
-    // group's). More than 256 columns leave no registers for either.
+    // With 16 warps two rows a step (b + grp and the next group's); more than 256 columns leave
+    // no registers for that.
     constexpr int kH = NL == 8 && NW == 16 ? 2 : 1;
-    constexpr bool kAhead = NL == 8;
     constexpr int kStep = kH * S::kRowStep;
-    float4 nx[kH][NL / 4];
-    auto fetch = [&](int b) {
-#pragma unroll
-      for (int h = 0; h < kH; ++h) {
-        const int r = b + h * S::kGroups + grp;
-        if (r < P.resident && r < n) {
-          const float4* src = reinterpret_cast<const float4*>(u_res + static_cast<int64_t>(r) * S::kCols);
-#pragma unroll
-          for (int q = 0; q < NL / 4; ++q) nx[h][q] = src[LPT * q + l];
-        } else if (r < n) {
-          const float4* src = reinterpret_cast<const float4*>(
-              u_spill + static_cast<int64_t>(r - P.resident) * S::kCols);
-#pragma unroll
-          for (int q = 0; q < NL / 4; ++q) nx[h][q] = __ldcg(src + LPT * q + l);
-        } else {
-#pragma unroll
-          for (int q = 0; q < NL / 4; ++q)
-            nx[h][q] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        }
-      }
-    };
     const int b0 = warp * kH * S::kGroups;
-    if (kAhead && b0 < n) fetch(b0);
-    for (int b = b0; b < n; b += kStep) {
-      if (!kAhead) fetch(b);
-      float4 u[kH][NL / 4];
-#pragma unroll
-      for (int h = 0; h < kH; ++h)
-#pragma unroll
-        for (int q = 0; q < NL / 4; ++q) u[h][q] = nx[h][q];
-      if (kAhead && b + kStep < n) fetch(b + kStep);
+    // u: the step's rows, r0 the first of them, n0 the end of the rows it is taken from
+    auto step = [&](const float4 (*u)[NL / 4], int r0, int n0) {
       float e[kH][NL], sum[kH], extra[kH];
       bal_rows<NL, LPT, kH>(u, gm, e, sum, extra);
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
-        const int r = b + h * S::kGroups + grp;
         // One correction of the quick quotient: its error has a sign, and one that all rows share
         // would move every gamma the same way in every iteration.
-        float w = sum[h] == 0.0f ? 0.0f : __fdividef(static_cast<float>(E), sum[h]);
+        float w = __fdividef(static_cast<float>(E), sum[h]);
         w = fmaf(w * inv_e, fmaf(-w, sum[h], static_cast<float>(E)), w);
         if (sum[h] == 0.0f) w = 0.0f;
         const u64 w2 = pk(w, w);
@@ -393,19 +365,81 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
           const u64 a = fma2(pk(e[h][i], e[h][i + 1]), w2, pk(acc[i], acc[i + 1]));
           upk(a, acc[i], acc[i + 1]);
         }
-        if (last && r < n && l == 0)
-          P.f[row0 + r] = sum[h] == 0.0f
-                              ? 0.0f
-                              : static_cast<float>(-bal_log2(sum[h] * inv_e, off, extra[h]) / ke);
+        if (last) {
+          const int r = r0 + h * S::kGroups + grp;
+          if (l == 0 && r < n0)
+            P.f[row0 + r] = sum[h] == 0.0f
+                                ? 0.0f
+                                : static_cast<float>(-bal_log2(sum[h] * inv_e, off, extra[h]) / ke);
+        }
+      }
+    };
+    const float4 closed = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    const int n_res = n < P.resident ? n : P.resident;
+    {
+      const float4* src = reinterpret_cast<const float4*>(u_res) + (b0 + grp) * S::kQuads + l;
+      for (int b = b0; b < n_res; b += kStep, src += kStep * S::kQuads) {
+        float4 u[kH][NL / 4];
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int q = 0; q < NL / 4; ++q)
+            u[h][q] = S::kGroups * kH == 1 || b + h * S::kGroups + grp < n_res
+                          ? src[h * S::kGroups * S::kQuads + LPT * q]
+                          : closed;
+        step(u, b, n_res);
       }
     }
-    // the CTA's column sums: rows of a warp, then the warps in their order
+    if constexpr (!CLUSTER) {
+      // the rows in the workspace, read one step ahead
+      const int n_sp = n - n_res;
+      const float4* src = reinterpret_cast<const float4*>(u_spill) + (b0 + grp) * S::kQuads + l;
+      float4 nx[kH][NL / 4];
+      auto fetch = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
+        for (int h = 0; h < kH; ++h)
 #pragma unroll
-      for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (grp == 0) csum[warp * S::kCols + S::column(l, i)] = acc[i];
+          for (int q = 0; q < NL / 4; ++q)
+            nx[h][q] = S::kGroups * kH == 1 || b + h * S::kGroups + grp < n_sp
+                           ? __ldcg(src + h * S::kGroups * S::kQuads + LPT * q)
+                           : closed;
+      };
+      if (b0 < n_sp) fetch(b0);
+      for (int b = b0; b < n_sp; b += kStep) {
+        float4 u[kH][NL / 4];
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int q = 0; q < NL / 4; ++q) u[h][q] = nx[h][q];
+        src += kStep * S::kQuads;
+        if (b + kStep < n_sp) fetch(b + kStep);
+        step(u, n_res + b, n);
+      }
     }
+    // the CTA's column sums: the rows of a warp (in each exchange a lane keeps half of its
+    // columns and its partner the other half, until one is left), then the warps in their order
+    int first = 0, kept = NL;  // the columns that this lane still holds: acc[0 .. kept - 1]
+    bool writes = true;
+#pragma unroll
+    for (int o = LPT; o < 32; o <<= 1) {
+      if (kept > 1) {
+        const bool up = (lane & o) != 0;
+        kept /= 2;
+#pragma unroll
+        for (int i = 0; i < NL / 2; ++i)
+          if (i < kept) {
+            const float send = up ? acc[i] : acc[i + kept];
+            acc[i] = (up ? acc[i + kept] : acc[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        if (up) first += kept;
+      } else {
+        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        writes = writes && (lane & o) == 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (i < kept && writes) csum[warp * S::kCols + S::column(l, first + i)] = acc[i];
     if (tid == 0) redo_sh = 0;
     __syncthreads();
     if constexpr (CLUSTER) {
@@ -439,8 +473,9 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
         }
       }
       if (it == 0) {
-        for (int q = 0; q < G; ++q) open_rows += part[q * kPartCols + S::kCols];
-        open_rows = fmaxf(open_rows, 1.0f);  // (no open row at all: f = g = 0)
+        double o2 = 0.0;
+        for (int q = 0; q < G; ++q) o2 += part[q * kPartCols + S::kCols];
+        inv_open = 1.0 / fmax(o2, 1.0);  // (no open row at all: f = g = 0)
       }
     } else {
       float* part = P.part + static_cast<int64_t>(it & 1) * G * kPartCols;
@@ -457,7 +492,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
         double o = 0.0;
         for (int q = 0; q < G; ++q)
           o += __ldcg(part + static_cast<int64_t>(q) * kPartCols + S::kCols);
-        open_rows = static_cast<float>(fmax(o, 1.0));
+        inv_open = 1.0 / fmax(o, 1.0);
       }
       // every CTA adds all CTAs' sums in the same order: four columns a thread, kParts strided
       // parts of the CTAs, then (below) the parts
@@ -483,7 +518,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
 #pragma unroll
         for (int pt = 0; pt < kParts; ++pt) c += csum[pt * S::kCols + j];
       }
-      c /= open_rows;
+      c = static_cast<float>(c * inv_open);
       csum[j] = c;  // (each thread rewrites only what it alone has read: part 0 of its column)
       if (lb[j] == -INFINITY) {
         gam[j] = -INFINITY;  // nothing is wanted of this column
@@ -549,7 +584,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
         }
         // a column closed to every row keeps g = 0
         gam[j] = cm == -INFINITY ? lb[j]
-                                 : -(cm + log2f(cl / open_rows)) + lb[j];
+                                 : -(cm + log2f(static_cast<float>(cl * inv_open))) + lb[j];
       }
       __syncthreads();
     }

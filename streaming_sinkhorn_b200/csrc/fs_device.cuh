@@ -204,7 +204,7 @@ __device__ __forceinline__ void st_async_cluster(float* local, unsigned rank, fl
 // Bounded wait for a phase of an mbarrier that other CTAs of the cluster complete, with
 // acquire semantics at cluster scope (their stores are then visible here).
 __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_ns();
+  unsigned long long t0 = 0;  // (the clock is read once the first try has failed)
   while (true) {
     uint32_t done;
     asm volatile(
@@ -215,7 +215,10 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_
         : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
         : "memory");
     if (done) return true;
-    if (global_ns() - t0 > kWaitLimitNs) return false;
+    if (t0 == 0)
+      t0 = global_ns();
+    else if (global_ns() - t0 > kWaitLimitNs)
+      return false;
   }
 }
 
