@@ -285,7 +285,7 @@ constexpr int kRouteFew = 12;
 // NL: experts per lane, lane l holding l * NL .. + NL - 1. Dynamic shared memory: route_room
 // doubles per warp, then the CTA's load.
 template <typename T, int NL, bool SIG>
-__global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kernel(const RouteParams P) {
+__global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kernel(const __grid_constant__ RouteParams P) {
   extern __shared__ __align__(16) unsigned char route_smem[];
   constexpr int kind = SIG ? kScoreSigmoid : kScoreSoftmax;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -36,13 +36,15 @@ fs_status by_type(int32_t dtype, F&& f) {
   }
 }
 
-// CTAs per row of the forward pass. One read of the matrix wants about two CTAs on every SM;
-// with fewer rows than that a row is shared by a cluster, while each CTA keeps at least one
-// full round of vectors.
+// CTAs per row of the forward pass. Up to half as many rows as SMs, a row is shared by a cluster,
+// which shortens the way through it (128000 bf16: one row 12.7 -> 5.3 us, 16 rows 13.1 -> 6.2),
+// while each CTA keeps at least a round of vectors; from there on the rows alone fill the SMs,
+// and joining parts costs more than it gains (64 x 50257 fp32, 5 alternatives: 16.8 us with one
+// CTA a row, 22.0 with eight).
 int token_cluster(int64_t rows, int64_t cols, int vec) {
   const int64_t sms = current_sms();
   int c = 1;
-  while (c < kTokenMaxCluster && rows * c < 2 * sms &&
+  while (c < kTokenMaxCluster && rows * c * 2 <= sms &&
          cols >= 2ll * c * TokenShape<8>::kRound / kTokenUnroll * vec)
     c *= 2;
   return c;
@@ -97,11 +99,13 @@ fs_status token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
     const int c = token_cluster(z->rows, z->cols, Elem<T>::kVec);
-    // few rows: eight warps on each, for the shortest way through one; many: four, which pay a
-    // row's fixed costs half as often
-    if (P.rows * c < 4ll * current_sms())
-      return top > 0 ? launch_tokens<T, true, 8>(P, c, st) : launch_tokens<T, false, 8>(P, c, st);
-    return top > 0 ? launch_tokens<T, true, 4>(P, c, st) : launch_tokens<T, false, 4>(P, c, st);
+    // Eight warps on a row; four, which pay a row's fixed costs half as often, where there are
+    // many rows and no alternatives (4096 x 65536 bf16: 100 us against 105). Alternatives have
+    // each warp wait for the others more often, and want the shorter way (1531 x 50257 fp32, 5
+    // of them: 70 us against 87).
+    if (top > 0) return launch_tokens<T, true, 8>(P, c, st);
+    return P.rows * c < 4ll * current_sms() ? launch_tokens<T, false, 8>(P, c, st)
+                                            : launch_tokens<T, false, 4>(P, c, st);
   });
 }
 
