@@ -14,8 +14,9 @@
 // One launch does all iterations. Every CTA keeps its rows' u in shared memory in fp32 (the
 // rest, if they do not all fit, in the workspace, read through L2 one step ahead), a group of
 // lanes takes a row, two rows at a time, each lane holding the column sums of its columns in
-// registers. All rows of a CTA share one offset in place of m_i, the largest u of the CTA plus
-// the largest gamma, so a row needs one reduction; a row whose sum comes out below 2^-60 is done
+// registers. All rows of a CTA share one offset
+// in place of m_i (none at all while the largest u of the CTA plus the largest gamma is in range
+// of ex2), so a row needs one reduction; a row whose sum comes out below 2^-60 is done
 // over with its own maximum. Per iteration the CTAs exchange one row of column sums each:
 // through distributed shared memory in a cluster of up to 16 CTAs when the whole problem fits
 // into their shared memory, else through the workspace and a grid barrier. That launch is
@@ -341,6 +342,10 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     }
     off = group_max<LPT>(off);
     off = (off == -INFINITY ? 0.0f : off) + umax;
+    // No u + gamma lies above off. 2^100 and sums of 1024 such terms are within range, so up to
+    // there no offset is taken at all: gamma less a large offset would lose digits of every
+    // column's gamma in every iteration (1e-6 of g at eps = 2 / experts).
+    off = off > 100.0f ? off - 100.0f : off < -20.0f ? off : 0.0f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) gm[i] = static_cast<float>(gam[S::column(l, i)] - off);
     // With 16 warps two rows a step (b + grp and the next group's); more than 256 columns leave
