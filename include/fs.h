@@ -522,10 +522,10 @@ FS_API fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt,
  *   g <- g_init (or 0);  repeat n_iters (1 .. 10^6) times:
  *     f_i <- -eps log sum_j b_j e^((s_ij + g_j)/eps),   b_j = load_j / sum load
  *     g_j <- -eps log mean_i e^((s_ij + f_i)/eps)
- * f (rows), g (experts; may alias g_init), float32. The plan b_j e^((s_ij + f_i + g_j)/eps) / rows has the load's
- * column sums, and its largest entry in a row is where s_ij + g_j + eps log b_j is: with that
- * bias (g alone for a uniform load) fs_route's first pick follows the load as far as the plan
- * is sharp (small eps); for k > 1 the further picks are evened out only roughly.
+ * f (rows), g (experts; may alias g_init), float32. The plan b_j e^((s_ij + f_i + g_j)/eps) / rows
+ * has the load's column sums, and its largest entry in a row is where s_ij + g_j + eps log b_j
+ * is: with that bias (g alone for a uniform load) fs_route's first pick follows the load as far
+ * as the plan is sharp (small eps); for k > 1 the further picks are evened out only roughly.
  * Logits of -inf are closed (e^.. = 0), a row of nothing else takes no part and gets f = 0, a
  * column closed to every row g = 0, a column of load 0 g = -inf. NaN in z, or a load with a
  * negative entry, NaN or sum 0, makes the outputs NaN. All iterations run in one cooperative
