@@ -11,11 +11,12 @@
 // a weight: those would cancel. A column whose c_j comes out below 2^-40 (its terms may have
 // been flushed) is done over with its own maximum.
 //
-// One launch does all iterations. Every CTA keeps its rows' u in shared memory in fp32 (the
-// rest, if they do not all fit, in the workspace, read through L2 one step ahead), a group of
-// lanes takes a row, two rows at a time, each lane holding the column sums of its columns in
-// registers. All rows of a CTA share one offset
-// in place of m_i (none at all while the largest u of the CTA plus the largest gamma is in range
+// One launch does all iterations. Every CTA keeps its rows' u in fp32, in shared memory and, when
+// that is full, in the SM's tensor memory, which has no products to serve here (the rest, if
+// they do not all fit, in the workspace, read through L2 one step ahead). A group of lanes takes
+// a row, two rows at a time, each lane holding the column sums of its columns in registers. All
+// rows of a CTA share one offset in place of m_i (none at all while the largest u of the CTA plus
+// the largest gamma is in range
 // of ex2), so a row needs one reduction; a row whose sum comes out below 2^-60 is done
 // over with its own maximum. Per iteration the CTAs exchange one row of column sums each:
 // through distributed shared memory in a cluster of up to 16 CTAs when the whole problem fits
@@ -26,6 +27,7 @@
 
 #include "fs_rowload.cuh"
 #include "fs_route.cuh"
+#include "fs_tcgen05.cuh"
 
 namespace fs {
 
@@ -44,7 +46,7 @@ struct BalanceParams {
   int32_t score;
   int32_t n_iters;
   int32_t per_cta;   // rows of a CTA
-  int32_t resident;  // of them, rows kept in shared memory
+  int32_t resident;  // of them, rows kept in shared memory; the next ones are in tensor memory
   float eps;
   const float* load;    // or NULL: uniform
   const float* g_init;  // or NULL: 0
@@ -91,6 +93,10 @@ struct BalShape {
   static constexpr int kCols = NL * LPT;
   static constexpr int kGroups = 32 / LPT;               // rows a warp takes at once
   static constexpr int kRowStep = kGroups * NW;          // rows a CTA takes at once
+  // Steps whose rows tensor memory holds: the NW / 4 warps of a lane quarter share its 512
+  // columns, a lane's NL columns of a row lie in as many of its own TMEM lane.
+  static constexpr int kTmemWarp = 512 / (NW / 4);
+  static constexpr int kTmemSteps = kTmemWarp / NL;
   static __host__ __device__ constexpr int column(int l, int i) {
     return 4 * (LPT * (i / 4) + l) + i % 4;
   }
@@ -210,6 +216,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
   __shared__ float warp_sh[2][NW];
   __shared__ uint64_t part_bar[2];  // CLUSTER: all CTAs' sums have arrived (by parity)
   __shared__ int redo_sh;
+  __shared__ uint32_t tmem_sh;
   // gamma is carried in 64 bits: it is a sum over the iterations, and next to 20 (eps = 0.05) a
   // float's rounding would show in g
   double* gam = bal_smem;                                  // [cols]
@@ -232,6 +239,30 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     return r < P.resident ? u_res + static_cast<int64_t>(r) * S::kCols
                           : u_spill + static_cast<int64_t>(r - P.resident) * S::kCols;
   };
+
+  // Rows that tensor memory holds (the workspace has them too, for columns done over). The CTA
+  // takes all of it and never waits for it: its registers fill the SM, so no other is on it.
+  const int n_tm = CLUSTER || n <= P.resident
+                       ? 0
+                       : (n - P.resident < S::kTmemSteps * S::kRowStep
+                              ? n - P.resident
+                              : S::kTmemSteps * S::kRowStep);
+  uint32_t tmem = 0;
+  if constexpr (!CLUSTER) {
+    if (n_tm > 0) {
+      if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+            smem_u32(&tmem_sh)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+      }
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      // this warp's lanes and columns
+      tmem = tmem_sh + (static_cast<uint32_t>(warp & 3) << 21) +
+             static_cast<uint32_t>((warp >> 2) * S::kTmemWarp);
+    }
+  }
 
   // log2 beta, gamma of the start
   if (warp == 0) {
@@ -316,6 +347,26 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     warp_sh[1][warp] = umax;
   }
   __syncthreads();
+  if constexpr (!CLUSTER) {
+    for (int b = warp * S::kGroups, q0 = 0; b < n_tm; b += S::kRowStep, q0 += NL) {
+      const int r = b + grp;  // (written by any warp, before the barrier)
+      const float4* src = reinterpret_cast<const float4*>(u_spill) + r * S::kQuads + l;
+      float v[NL];
+#pragma unroll
+      for (int q = 0; q < NL / 4; ++q) {
+        const float4 x = r < n_tm ? src[LPT * q]
+                                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        v[4 * q] = x.x;
+        v[4 * q + 1] = x.y;
+        v[4 * q + 2] = x.z;
+        v[4 * q + 3] = x.w;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < NL; q += 8) tc_st8(tmem + q0 + q, v + q);
+    }
+    tc_wait_st();
+  }
   umax = warp_maxf(lane < NW ? warp_sh[1][lane] : -INFINITY);
   if (umax == -INFINITY) umax = 0.0f;
 
@@ -396,9 +447,22 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
       }
     }
     if constexpr (!CLUSTER) {
+      static_assert(kH == 1, "a step of tensor memory is one row of each group");
+      for (int b = b0, q0 = 0; b < n_tm; b += kStep, q0 += NL) {
+        float v[NL];
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < NL; q += 8) tc_ld8(tmem + q0 + q, v + q);
+        float4 u[kH][NL / 4];
+#pragma unroll
+        for (int q = 0; q < NL / 4; ++q)
+          u[0][q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        step(u, n_res + b, n);
+      }
       // the rows in the workspace, read one step ahead
-      const int n_sp = n - n_res;
-      const float4* src = reinterpret_cast<const float4*>(u_spill) + (b0 + grp) * S::kQuads + l;
+      const int n_sp = n - n_res - n_tm;
+      const float4* src =
+          reinterpret_cast<const float4*>(u_spill) + (n_tm + b0 + grp) * S::kQuads + l;
       float4 nx[kH][NL / 4];
       auto fetch = [&](int b) {
 #pragma unroll
@@ -418,7 +482,7 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
           for (int q = 0; q < NL / 4; ++q) u[h][q] = nx[h][q];
         src += kStep * S::kQuads;
         if (b + kStep < n_sp) fetch(b + kStep);
-        step(u, n_res + b, n);
+        step(u, n_res + n_tm + b, n);
       }
     }
     // the CTA's column sums: the rows of a warp (in each exchange a lane keeps half of its
@@ -595,6 +659,15 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
     }
   }
   if (CLUSTER && G > 1) cluster_barrier();  // no CTA leaves while sums are on their way to it
+  if constexpr (!CLUSTER) {
+    if (n_tm > 0) {
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_sh));
+    }
+  }
   if (!alive) {
     for (int r = tid; r < n; r += S::kThreads) P.f[row0 + r] = __int_as_float(0x7FC00000);
     if (blockIdx.x == 0)

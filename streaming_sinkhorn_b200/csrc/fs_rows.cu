@@ -290,7 +290,7 @@ struct BalancePlan {
   size_t off_redo, off_spill, total;  // workspace: sync word, partial sums, redo, spill
 };
 
-constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 140 bytes
+constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 300 bytes
 
 BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   BalancePlan p{};
