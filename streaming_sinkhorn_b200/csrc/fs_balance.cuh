@@ -20,7 +20,7 @@
 // of ex2), so a row needs one reduction; a row whose sum comes out below 2^-60 is done
 // over with its own maximum. Per iteration the CTAs exchange one row of column sums each:
 // through distributed shared memory in a cluster of up to 16 CTAs when the whole problem fits
-// into their shared memory, else through the workspace and a grid barrier. That launch is
+// into their shared memory, else by integer atomics and a grid barrier. That launch is
 // cooperative, so all CTAs run at once, and its waits are bounded: when one expires the call's
 // outputs are NaN.
 #pragma once
@@ -36,6 +36,14 @@ constexpr int kBalGridWarps = 32;
 constexpr int kBalMaxCluster = 16;
 constexpr float kBalLowSum = 0x1p-60f;   // a row's sum that may have lost terms
 constexpr float kBalFlushed = 0x1p-40f;  // a column's mean that may have lost terms
+
+// Words of one iteration's column sums across the grid: copies (a CTA adds to one of them) of
+// high and low parts, a flag, the open rows.
+#ifndef BCOP
+#define BCOP 4
+#endif
+constexpr int kBalCopies = BCOP;
+__host__ __device__ constexpr int bal_sums(int cols) { return kBalCopies * 2 * cols + 2; }
 
 struct BalanceParams {
   const void* z;
@@ -53,7 +61,7 @@ struct BalanceParams {
   float* f;
   float* g;
   unsigned* sync;   // [0] arrivals, [1] nonzero once a wait has expired; zeroed before the launch
-  float* part;      // [2][gridDim][cols + 4] column sums (and open rows) by iteration parity
+  u64* sums;        // grid: [3][bal_sums] column sums in whole numbers, by iteration; zeroed, too
   float2* redo;     // [gridDim][cols] (max, sum) of columns done over
   float* spill;     // u of the rows beyond `resident`, (gridDim, per_cta - resident, cols)
 };
@@ -203,14 +211,38 @@ __device__ __forceinline__ double bal_log2(float v, float off, float extra) {
   return (static_cast<double>(off) + extra + k) + log2f(f);
 }
 
+// Column sums across the grid are added up by atomics on whole numbers, whose order does not
+// change the result: c in units of 2^-20 (c <= rows x experts < 2^41) and what that leaves in
+// units of 2^-60. Each CTA's part is off by less than 2^-60: of the smallest mean that counts
+// (2^-40) a part in 2^20 times the number of rows. NaN sets a flag.
+template <int C>  // padded columns; sums: [kBalCopies][2][C], then the flag
+__device__ __forceinline__ void bal_add(u64* sums, int j, float c) {
+  if (!(c < 0x1p42f)) {
+    sums[kBalCopies * 2 * C] = 1;  // (every CTA that writes it writes the same)
+    return;
+  }
+  const float hi = truncf(c * 0x1p20f);
+  sums += (blockIdx.x % kBalCopies) * 2 * C + j;
+  atomicAdd(sums, static_cast<u64>(hi));
+  atomicAdd(sums + C, static_cast<u64>(fmaf(hi, -0x1p-20f, c) * 0x1p60f));
+}
+template <int C>
+__device__ __forceinline__ double bal_sum(const u64* sums, int j) {
+  u64 hi = 0, lo = 0;
+#pragma unroll
+  for (int i = 0; i < kBalCopies; ++i) {
+    hi += __ldcg(sums + i * 2 * C + j);
+    lo += __ldcg(sums + i * 2 * C + C + j);
+  }
+  if (__ldcg(sums + kBalCopies * 2 * C) != 0) return __longlong_as_double(0x7FF8000000000000ll);
+  return static_cast<double>(hi) * 0x1p-20 + static_cast<double>(lo) * 0x1p-60;
+}
+
 template <typename T, int NL, int LPT, int NW, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams P) {
   using S = BalShape<NL, LPT, NW>;
   constexpr int kPartCols = S::kCols + 4;  // column sums, then the open rows
-  constexpr int kQuads = S::kQuads;
-  constexpr int kParts = kQuads >= S::kThreads ? 1 : (S::kThreads / kQuads < NW
-                                                          ? S::kThreads / kQuads
-                                                          : NW);
+  constexpr int kSums = bal_sums(S::kCols);
   extern __shared__ __align__(16) double bal_smem[];
   __shared__ int ok_sh;
   __shared__ float warp_sh[2][NW];
@@ -547,48 +579,36 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
         inv_open = 1.0 / fmax(o2, 1.0);  // (no open row at all: f = g = 0)
       }
     } else {
-      float* part = P.part + static_cast<int64_t>(it & 1) * G * kPartCols;
+      u64* sums = P.sums + (it % 3) * kSums;
       for (int j = tid; j <= S::kCols; j += S::kThreads) {
         float c = 0.0f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) c += j < S::kCols ? csum[w * S::kCols + j] : warp_sh[0][w];
-        part[static_cast<int64_t>(blockIdx.x) * kPartCols + j] = c;
+        if (j < E)
+          bal_add<S::kCols>(sums, j, c);
+        else if (j == S::kCols && it == 0)
+          atomicAdd(sums + kSums - 1, static_cast<u64>(c));
       }
       arrivals += G;
       alive = grid_barrier(P.sync, arrivals, &ok_sh);
       if (!alive) break;
-      if (it == 0) {
-        double o = 0.0;
-        for (int q = 0; q < G; ++q)
-          o += __ldcg(part + static_cast<int64_t>(q) * kPartCols + S::kCols);
-        inv_open = 1.0 / fmax(o, 1.0);
-      }
-      // every CTA adds all CTAs' sums in the same order: four columns a thread, kParts strided
-      // parts of the CTAs, then (below) the parts
-      for (int w = tid; w < kParts * kQuads; w += S::kThreads) {
-        const int j = w % kQuads, pt = w / kQuads;
-        float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 10
-        for (int q = pt; q < G; q += kParts) {
-          const float4 x = __ldcg(
-              reinterpret_cast<const float4*>(part + static_cast<int64_t>(q) * kPartCols) + j);
-          c = make_float4(c.x + x.x, c.y + x.y, c.z + x.z, c.w + x.w);
-        }
-        reinterpret_cast<float4*>(csum)[w] = c;
-      }
-      __syncthreads();
+      // all CTAs have read the sums of the iteration before, and none adds to their place before
+      // the next barrier
+      if (blockIdx.x == 0)
+        for (int j = tid; j < kSums; j += S::kThreads) P.sums[(it + 2) % 3 * kSums + j] = 0;
+      if (it == 0)
+        inv_open = 1.0 / fmax(static_cast<double>(__ldcg(sums + kSums - 1)), 1.0);
     }
     for (int j = tid; j < E; j += S::kThreads) {
       float c = 0.0f;
       if constexpr (CLUSTER) {
         const float* part = parts + (it & 1) * kBalMaxCluster * kPartCols + j;
         for (int q = 0; q < G; ++q) c += part[q * kPartCols];
+        c = static_cast<float>(c * inv_open);
       } else {
-#pragma unroll
-        for (int pt = 0; pt < kParts; ++pt) c += csum[pt * S::kCols + j];
+        c = static_cast<float>(bal_sum<S::kCols>(P.sums + (it % 3) * kSums, j) * inv_open);
       }
-      c = static_cast<float>(c * inv_open);
-      csum[j] = c;  // (each thread rewrites only what it alone has read: part 0 of its column)
+      csum[j] = c;  // (all sums over the warps have been read)
       if (lb[j] == -INFINITY) {
         gam[j] = -INFINITY;  // nothing is wanted of this column
       } else if (c < kBalFlushed) {

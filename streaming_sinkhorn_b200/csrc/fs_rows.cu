@@ -287,7 +287,7 @@ struct BalancePlan {
   bool cluster;  // one cluster, everything in shared memory
   int ctas, per_cta, resident;
   size_t smem;
-  size_t off_redo, off_spill, total;  // workspace: sync word, partial sums, redo, spill
+  size_t off_redo, off_spill, total;  // workspace: sync word, column sums, redo, spill
 };
 
 constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 300 bytes
@@ -330,7 +330,7 @@ BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   p.resident = static_cast<int>(std::min<int64_t>(p.per_cta, (kBalSmemBudget - used) / row));
   p.smem = used + p.resident * row;
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
-  p.off_redo = 256 + up(2 * static_cast<size_t>(p.ctas) * (p.cols + 4) * 4);
+  p.off_redo = 256 + up(3 * static_cast<size_t>(bal_sums(p.cols)) * sizeof(u64));
   p.off_spill = p.off_redo + up(static_cast<size_t>(p.ctas) * p.cols * 8);
   p.total = p.off_spill + up(static_cast<size_t>(p.ctas) * (p.per_cta - p.resident) * row);
   return p;
@@ -437,11 +437,11 @@ fs_status balance(const fs_matrix* z, int32_t score, float eps, int32_t n_iters,
   P.f = f;
   P.g = g;
   P.sync = reinterpret_cast<unsigned*>(base);
-  P.part = reinterpret_cast<float*>(base + 256);
+  P.sums = reinterpret_cast<u64*>(base + 256);
   P.redo = reinterpret_cast<float2*>(base + p.off_redo);
   P.spill = reinterpret_cast<float*>(base + p.off_spill);
-  if (!p.cluster) {  // the grid barrier's word
-    s = cuda_status(cudaMemsetAsync(base, 0, 256, st), "cudaMemsetAsync");
+  if (!p.cluster) {  // the grid barrier's word and the column sums
+    s = cuda_status(cudaMemsetAsync(base, 0, p.off_redo, st), "cudaMemsetAsync");
     if (s != FS_OK) return s;
   }
   return by_type(z->dtype, [&](auto* t) -> fs_status {
