@@ -292,6 +292,8 @@ struct BalancePlan {
 
 constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 300 bytes
 
+constexpr int64_t kBalClusterScores = 640 * 1000;  // (balance_plan says why)
+
 BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   BalancePlan p{};
   p.nl = experts <= 256 ? 8 : experts <= 512 ? 16 : 32;
@@ -307,11 +309,13 @@ BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
     p.per_cta = static_cast<int>(per);
     p.ctas = static_cast<int>(std::max<int64_t>(1, (rows + per - 1) / per));
   };
-  // A cluster exchanges its sums faster than the grid meets at a barrier, so one is taken whenever
-  // its shared memory holds the problem, with fewer CTAs for fewer rows (10 iterations: 512 x 16
-  // 20 us against 45, 8191 x 64 43 against 55, 12000 x 64 54 against 61).
+  // A cluster exchanges its sums in less time than the grid's 4 us an iteration, but has only 16
+  // SMs: it is taken, with fewer CTAs for fewer rows, while the exponentials of one iteration on
+  // those take less than what it saves, and shared memory holds them (10 iterations, us, cluster
+  // and grid: 512 x 16 20 and 43, 2048 x 64 26 and 47, 1000 x 256 40 and 48, 8191 x 64 44 and 48,
+  // 40000 x 16 46 and 49, 2000 x 256 51 and 49, 12000 x 64 54 and 49).
   p.cluster = false;
-  if (allow_cluster && p.nl == 8) {
+  if (allow_cluster && p.nl == 8 && rows * p.cols <= kBalClusterScores) {
     for (int c = 1; c <= kBalMaxCluster && !p.cluster; c *= 2) {
       if (c < kBalMaxCluster && rows > 2 * step * c) continue;
       if ((rows + c - 1) / c * row + cluster_fixed > kBalSmemBudget) continue;

@@ -488,6 +488,32 @@ def test_balance_rows_beyond_shared_memory():
     check_balance(z, 0.1, 3, "sigmoid")
 
 
+@pytest.mark.parametrize("rows,experts", [(200003, 60), (70001, 250), (20000, 500), (15500, 1000)])
+def test_balance_rows_in_and_beyond_tensor_memory(rows, experts):
+    """Rows that fill part of a step of tensor memory, and rows that pass it, for rows of part of
+    a warp, of a warp, and of several quads a lane."""
+    z = rand(rows, experts, seed=65, scale=1.0)
+    check_balance(z, 0.1, 2, "sigmoid")
+
+
+def test_balance_unkind_rows_across_the_grid():
+    z = rand(30011, 64, seed=66, scale=1.0)
+    load = torch.arange(64, dtype=F32, device="cuda")
+    g0 = rand(64, seed=67, scale=0.1)
+    z[:, 5] = -math.inf
+    z[7:2000] = -math.inf
+    f, g = check_balance(z, 0.2, 3, "sigmoid", load=load, g_init=g0)
+    assert g[0].item() == -math.inf and g[5].item() == 0.0 and f[7].item() == 0.0
+    z[1:] = -math.inf  # a single row takes part
+    check_balance(z, 0.2, 3, "softmax")
+    # columns whose terms underflow next to the rows' largest
+    z = torch.linspace(-6, 6, 60, device="cuda").repeat(20000, 1) + rand(20000, 60, seed=68, scale=0.01)
+    check_balance(z, 0.003, 3, "sigmoid")
+    z[19999, 3] = math.nan
+    f, g = fs.balance(z, eps=0.1, n_iters=3)
+    assert f.isnan().all() and g.isnan().all()
+
+
 def test_balance_load_start_and_closed():
     z = rand(300, 24, seed=62, scale=1.0)
     z[7] = -math.inf
