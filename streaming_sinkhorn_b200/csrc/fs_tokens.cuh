@@ -565,8 +565,7 @@ __global__ void __launch_bounds__(kTokenGradThreads)
   constexpr int V = Elem<T>::kVec, U = kTokenUnroll;
   constexpr int64_t kChunk = static_cast<int64_t>(kTokenGradThreads) * U * V;
   const int tid = threadIdx.x;
-  // the last rows first: after a forward pass they are the ones still in L2
-  const int64_t row = P.rows - 1 - blockIdx.x / P.chunks;
+  const int64_t row = blockIdx.x / P.chunks;
   const int chunk = static_cast<int>(blockIdx.x % P.chunks);
   const T* z = static_cast<const T*>(P.z) + row * P.ld;
   T* out = static_cast<T*>(P.grad) + row * P.ld_grad;
