@@ -99,13 +99,16 @@ fs_status token_logprobs(const fs_matrix* z, float eps, const void* ids, int32_t
   return by_type(z->dtype, [&](auto* t) -> fs_status {
     using T = std::remove_pointer_t<decltype(t)>;
     const int c = token_cluster(z->rows, z->cols, Elem<T>::kVec);
-    // Eight warps on a row; four, which pay a row's fixed costs half as often, where there are
-    // many rows and no alternatives (4096 x 65536 bf16: 100 us against 105). Alternatives have
-    // each warp wait for the others more often, and want the shorter way (1531 x 50257 fp32, 5
-    // of them: 70 us against 87).
-    if (top > 0) return launch_tokens<T, true, 8>(P, c, st);
-    return P.rows * c < 4ll * current_sms() ? launch_tokens<T, false, 8>(P, c, st)
-                                            : launch_tokens<T, false, 4>(P, c, st);
+    // Eight warps on a row; four, which pay a row's fixed costs with twice as many CTAs, where
+    // there are many rows (4096 x 65536 bf16 100 us against 105; with 5 alternatives 16384 x 1000
+    // bf16 149 against 249). Alternatives have each warp wait for the others more often and want
+    // the shorter way up to more rows (1531 x 50257 fp32, 5 of them: 72 us against 86).
+    const int64_t many = (top > 0 ? 16ll : 4ll) * current_sms();
+    if (top > 0)
+      return P.rows * c < many ? launch_tokens<T, true, 8>(P, c, st)
+                               : launch_tokens<T, true, 4>(P, c, st);
+    return P.rows * c < many ? launch_tokens<T, false, 8>(P, c, st)
+                             : launch_tokens<T, false, 4>(P, c, st);
   });
 }
 

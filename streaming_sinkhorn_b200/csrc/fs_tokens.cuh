@@ -12,9 +12,10 @@
 // and writes the matrix once (158 us, 6.8 TB/s).
 //
 // Order of alternatives: larger z first, equal z by the lower index. The first round of a row
-// gives a bar that at least `top` scores reach; a warp sets the few vectors that reach it aside
-// and looks at their scores later, keeping its best (value, index) pairs as whole numbers sorted
-// across its lanes; the warps' lists are joined at the row's end.
+// gives a bar that at least `top` scores reach; a warp sets the few vectors that reach it aside,
+// and at the row's end all scores that do are (value, index) pairs, as whole numbers, in shared
+// memory, where each counts those above it. A warp that has set aside too many looks at them
+// meanwhile and keeps its best pairs sorted across its lanes.
 //
 // A row is read by one CTA, or by a cluster of up to 8 when there are few rows (a decoding
 // step), whose partial results meet in the first CTA through distributed shared memory: one
@@ -178,6 +179,8 @@ __device__ __forceinline__ u64 token_offer(u64 list, u64 key, int top, int lane)
   return list;
 }
 
+constexpr int kTokenFew = 6;  // alternatives whose bar is merged one by one
+
 // Vectors that reach the bar, kept by a warp until it looks at their scores.
 constexpr int kTokenKept = 64;
 
@@ -201,9 +204,10 @@ template <int NW>
 struct TokenTop {  // alternatives
   uint4 kept[NW][kTokenKept];
   int kept_at[NW][kTokenKept];  // a vector's first column
-  u64 best[NW][32];
-  uint32_t maxima[NW][32];
-  u64 total_best[32];
+  uint32_t maxima[64];
+  u64 best[NW][32];  // a warp's pairs, in no order
+  int count[NW];
+  u64 total_best[32];  // the CTA's, sorted
 };
 struct TokenNoTop {};
 
@@ -213,35 +217,57 @@ __device__ __forceinline__ void token_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
 }
 
-// The bar of a row after its first round: the top-th largest of all threads' maxima (bm; have:
-// this thread has read a vector). At least `top` scores lie at or above it, and in a row of n
-// scores in random order about top * n / (scores of the round) do. Called by all computing
-// warps; each sorts its lanes' maxima out by `top` reductions, then merges the warps' lists.
+// The bar of a row after its first round of `vectors`, a score that at least `top` of its scores
+// reach: the top-th largest of the warps' m largest thread maxima (bm; have: this thread has read
+// a vector). A few are merged one by one; for more, two from each warp beyond its share, whose
+// top-th largest hardly ever lies below that of all, and each counts those above it (1 x 128000
+// bf16, 20 alternatives: 11.1 us, 12.7 one by one; with 5 the same, and 1531 x 50257 72 against
+// 75 by counting). Called by all computing warps.
 template <int NW>
-__device__ __forceinline__ float token_bar(float bm, bool have, int top, TokenTop<NW>& sh,
-                                           int warp, int lane) {
-  uint32_t mine = have && bm == bm ? order_key(bm) : 0u;
-  uint32_t sorted = 0u;
-  for (int r = 0; r < top; ++r) {
-    const uint32_t t = __reduce_max_sync(0xffffffffu, mine);
-    if (t == 0u) break;
-    if (lane == r) sorted = t;
+__device__ __noinline__ float token_bar(float bm, int vectors, bool have, int top,
+                                        TokenTop<NW>& sh, int warp, int lane) {
+  const int warps = min(NW, (vectors + 31) / 32);  // those that have read any
+  const bool few = top <= kTokenFew;
+  const int m = few ? top : min(top, (top + warps - 1) / warps + 2);
+  uint32_t mine = have && bm == bm ? order_key(bm) : 0u, t = 0u;
+  for (int r = 0; r < m; ++r) {
+    t = __reduce_max_sync(0xffffffffu, mine);
+    if (warp < warps && lane == 0) sh.maxima[warp * m + r] = t;
     // (equal maxima count one by one)
     if (lane == __ffs(__ballot_sync(0xffffffffu, mine == t)) - 1) mine = 0u;
   }
-  sh.maxima[warp][lane] = sorted;
+  const int n = warps * m;  // top .. 60
+  if (warp == 0 && lane < 4) sh.maxima[n + lane] = 0u;  // (read by fours)
   token_sync<NW>();
-  int next = 0;
-  uint32_t head = lane < NW ? sh.maxima[lane][0] : 0u, t = 0u;
-  for (int r = 0; r < top; ++r) {
-    t = __reduce_max_sync(0xffffffffu, head);
-    if (t == 0u) break;
-    if (lane == __ffs(__ballot_sync(0xffffffffu, head == t)) - 1) {
-      ++next;
-      head = next < 32 ? sh.maxima[lane][next] : 0u;
+  if (few) {
+    int next = lane * m;
+    uint32_t head = lane < warps ? sh.maxima[next] : 0u;
+    for (int r = 0; r < top; ++r) {
+      t = __reduce_max_sync(0xffffffffu, head);
+      if (t == 0u) break;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, head == t)) - 1) {
+        ++next;
+        head = next < (lane + 1) * m ? sh.maxima[next] : 0u;
+      }
     }
+  } else {
+    const uint32_t x = lane < n ? sh.maxima[lane] : 0u;
+    const uint32_t y = lane + 32 < n ? sh.maxima[lane + 32] : 0u;
+    int px = 0, py = 0;  // places: equal ones in their order
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sh.maxima + i);
+      const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        px += v[e] > x || (v[e] == x && i + e < lane) ? 1 : 0;
+        py += v[e] > y || (v[e] == y && i + e < lane + 32) ? 1 : 0;
+      }
+    }
+    const uint32_t hit = lane < n && px == top - 1 ? x : lane + 32 < n && py == top - 1 ? y : 0u;
+    t = __reduce_max_sync(0xffffffffu, hit);
   }
-  // with fewer than `top` maxima everything counts, -inf included
+  // with fewer maxima everything counts, -inf included
   return t != 0u ? order_unkey(t) : -INFINITY;
 }
 
@@ -273,6 +299,85 @@ __device__ __noinline__ u64 token_look(u64 list, float& bar, const uint4* kept, 
   const u64 last = __shfl_sync(0xffffffffu, list, top - 1);
   if (last) bar = fmaxf(bar, token_key_value(last));
   return list;
+}
+
+// The scores of the warp's `n` (up to 32) kept vectors that reach the bar, as pairs in no order:
+// their number, the first 32 of them in `out`.
+template <typename T>
+__device__ __forceinline__ int token_give(float bar, const uint4* kept, const int* kept_at, int n,
+                                       u64* out, int lane) {
+  constexpr int V = Elem<T>::kVec;
+  const unsigned below = (1u << lane) - 1u;
+  __syncwarp();
+  float f[V];
+  Elem<T>::unpack(kept[lane < n ? lane : 0], f);
+  const int at = kept_at[lane < n ? lane : 0];
+  int count = 0;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const bool reach = lane < n && f[e] >= bar;
+    const unsigned who = __ballot_sync(0xffffffffu, reach);
+    const int to = count + __popc(who & below);
+    if (reach && to < 32) out[to] = token_key(f[e], at + e);
+    count += __popc(who);
+  }
+  return count;
+}
+
+// The end of a row for a warp: its scores that reach the bar (of warp 0 the unaligned ends too)
+// become its pairs in shared memory, in no order; if there are more than 32, its best ones.
+template <typename T, int NW>
+__device__ __noinline__ void token_finish(u64 list, float bar, int kept, TokenTop<NW>& best,
+                                          bool hd, float zh, bool tl, float zt, int tail, int top,
+                                          int warp, int lane) {
+  int n = 0;
+  const bool looked = __any_sync(0xffffffffu, list != 0);
+  if (!looked) {
+    if (kept > 0)
+      n = token_give<T>(bar, best.kept[warp], best.kept_at[warp], kept, best.best[warp], lane);
+    if (warp == 0) {
+      const bool rh = hd && zh >= bar, rt = tl && zt >= bar;
+      const unsigned wh = __ballot_sync(0xffffffffu, rh), wt = __ballot_sync(0xffffffffu, rt);
+      const unsigned below = (1u << lane) - 1u;
+      const int th = n + __popc(wh & below), tt = n + __popc(wh) + __popc(wt & below);
+      if (rh && th < 32) best.best[0][th] = token_key(zh, lane);
+      if (rt && tt < 32) best.best[0][tt] = token_key(zt, tail + lane);
+      n += __popc(wh) + __popc(wt);
+    }
+  }
+  if (looked || n > 32) {
+    list = token_look<T>(list, bar, best.kept[warp], best.kept_at[warp], kept, top, lane);
+    if (warp == 0) {
+      list = token_offer(list, hd && zh == zh ? token_key(zh, lane) : 0ull, top, lane);
+      list = token_offer(list, tl && zt == zt ? token_key(zt, tail + lane) : 0ull, top, lane);
+    }
+    n = __popc(__ballot_sync(0xffffffffu, lane < top && list != 0));
+    best.best[warp][lane] = list;
+  }
+  __syncwarp();
+  if (lane >= n && lane < max(4, n + (n & 1))) best.best[warp][lane] = 0;  // (read in pairs)
+  if (lane == 0) best.count[warp] = n;
+  if (warp == 0) best.total_best[lane] = 0;
+}
+
+// How many of all warps' pairs are above `key`. Every warp's list ends with a 0 or at 32, and has
+// 4 entries at least.
+template <int NW>
+__device__ __noinline__ int token_place(u64 key, const u64 (*best)[32], const int* count) {
+  int place = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&best[w][0]);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&best[w][2]);
+    place += (a.x > key ? 1 : 0) + (a.y > key ? 1 : 0) + (b.x > key ? 1 : 0) + (b.y > key ? 1 : 0);
+  }
+#pragma unroll 1
+  for (int w = 0; w < NW; ++w)
+    for (int i = 4; i < count[w]; i += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&best[w][i]);
+      place += (o.x > key ? 1 : 0) + (o.y > key ? 1 : 0);
+    }
+  return place;
 }
 
 // The part of a row that a CTA reads: `nvec` vectors from element `head` on are shared by the
@@ -409,7 +514,7 @@ __global__ void __launch_bounds__(NW * 32 + 32, NW == 8 ? (TOP ? 3 : 4) : (TOP ?
       for (int u = 1; u < U; ++u) bm = fmaxf(bm, vmax[u]);
       token_add<U * V>(s, f, bm, k2);
       if constexpr (TOP) {
-        if (b == p.v0) bar = token_bar<NW>(bm, left > 0, P.top, best, warp, lane);
+        if (b == p.v0) bar = token_bar<NW>(bm, p.v1 - b, left > 0, P.top, best, warp, lane);
         if (__any_sync(0xffffffffu, bm >= bar)) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
@@ -432,41 +537,33 @@ __global__ void __launch_bounds__(NW * 32 + 32, NW == 8 ? (TOP ? 3 : 4) : (TOP ?
         }
       }
     }
-    if constexpr (TOP)
-      list = token_look<T>(list, bar, best.kept[warp], best.kept_at[warp], kept, P.top, lane);
-    if (warp == 0) {  // the unaligned ends: at most 7 scores each
-      const int tail = p.head + p.nvec * V;
-      const bool hd = rank == 0 && lane < p.head;
-      const bool tl = rank == cluster - 1 && lane < P.cols - tail;
-      const float zh = hd ? Elem<T>::to_f(z[lane]) : -INFINITY;
-      const float zt = tl ? Elem<T>::to_f(z[tail + lane]) : -INFINITY;
+    float zh = -INFINITY, zt = -INFINITY;  // the unaligned ends: at most 7 scores each
+    const int tail = p.head + p.nvec * V;
+    const bool hd = warp == 0 && rank == 0 && lane < p.head;
+    const bool tl = warp == 0 && rank == cluster - 1 && lane < P.cols - tail;
+    if (warp == 0) {
+      if (hd) zh = Elem<T>::to_f(z[lane]);
+      if (tl) zt = Elem<T>::to_f(z[tail + lane]);
       const float f[2] = {zh, zt};
       token_add<2>(s, f, fmaxf(zh, zt), k2);
-      if constexpr (TOP) {
-        list = token_offer(list, hd && zh == zh ? token_key(zh, lane) : 0ull, P.top, lane);
-        list = token_offer(list, tl && zt == zt ? token_key(zt, tail + lane) : 0ull, P.top, lane);
-      }
     }
+    if constexpr (TOP)
+      token_finish<T, NW>(list, bar, kept, best, hd, zh, tl, zt, tail, P.top, warp, lane);
 
     s = token_reduce<32>(s, k2);
     parity ^= 1;
     if (lane == 0) sh.sum[parity][warp] = s;
-    if constexpr (TOP) best.best[warp][lane] = list;
     token_sync<NW>();
     if constexpr (TOP) {
-      // pairs of warps join their lists, then pairs of pairs
-#pragma unroll 1
-      for (int half = NW / 2; half > 0; half >>= 1) {
-        if (warp < half) {
-          const u64 other = best.best[warp + half][lane];
-          // (lists may end below another's last kept key)
-          if (__any_sync(0xffffffffu, other > __shfl_sync(0xffffffffu, list, P.top - 1))) {
-            list = token_join(list, other, lane);
-            best.best[warp][lane] = list;
-          }
-        }
-        token_sync<NW>();
+      // every pair's place among all warps' (no two are equal)
+      const int n = best.count[warp];
+      if (n > 0) {
+        const u64 key = lane < n ? best.best[warp][lane] : 0ull;
+        const int place = token_place<NW>(key, best.best, best.count);
+        if (key != 0 && place < P.top) best.total_best[place] = key;
       }
+      token_sync<NW>();
+      if (warp == 0) list = best.total_best[lane];
     }
     if (warp == 0) {
       s = token_reduce<NW>(sh.sum[parity][lane % NW], k2);
@@ -476,23 +573,33 @@ __global__ void __launch_bounds__(NW * 32 + 32, NW == 8 ? (TOP ? 3 : 4) : (TOP ?
       cg::cluster_group cl = cg::this_cluster();
       if (warp == 0) {
         if (lane == 0) sh.total = s;
-        if constexpr (TOP) best.total_best[lane] = list;
       }
       cl.sync();  // (the copying warps leave by themselves)
-      if (rank == 0 && warp == 0) {
-        // lane c takes CTA c's sum
-        const int c0 = lane % kTokenMaxCluster;
-        s = token_reduce<kTokenMaxCluster>(c0 < cluster ? cl.map_shared_rank(&sh, c0)->total
-                                                        : TokenSum{-INFINITY, 0.0f, 0.0f},
-                                           k2);
+      if (rank == 0) {
         if constexpr (TOP) {
-          u64 o[kTokenMaxCluster];
-#pragma unroll
-          for (int c = 1; c < kTokenMaxCluster; ++c)
-            o[c] = c < cluster ? cl.map_shared_rank(&best, c)->total_best[lane] : 0ull;
-#pragma unroll
-          for (int c = 1; c < kTokenMaxCluster; ++c)
-            if (c < cluster) list = token_join(list, o[c], lane);
+          // the CTAs' lists by pairs, a warp each
+          static_assert(NW >= kTokenMaxCluster / 2, "a warp for each pair of lists");
+          if (2 * warp < cluster) {
+            list = token_join(cl.map_shared_rank(&best, 2 * warp)->total_best[lane],
+                              cl.map_shared_rank(&best, 2 * warp + 1)->total_best[lane], lane);
+            best.best[warp][lane] = list;
+          }
+          token_sync<NW>();
+#pragma unroll 1
+          for (int half = cluster / 4; half > 0; half >>= 1) {
+            if (warp < half) {
+              list = token_join(list, best.best[warp + half][lane], lane);
+              best.best[warp][lane] = list;
+            }
+            token_sync<NW>();
+          }
+        }
+        if (warp == 0) {
+          // lane c takes CTA c's sum
+          const int c0 = lane % kTokenMaxCluster;
+          s = token_reduce<kTokenMaxCluster>(c0 < cluster ? cl.map_shared_rank(&sh, c0)->total
+                                                          : TokenSum{-INFINITY, 0.0f, 0.0f},
+                                             k2);
         }
       }
       cl.sync();  // no CTA ends while its shared memory is read
