@@ -247,6 +247,11 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
           : launch_linear<256, 2, false, false, kLinLse>("fs_linear_logprobs", ma, mt, mb, P, sms, st);
   if (s != FS_OK) return s;
   LinJoinParams J{};
+  J.x = static_cast<const __nv_bfloat16*>(x->data);
+  J.w = static_cast<const __nv_bfloat16*>(w->data);
+  J.ld_x = x->ld;
+  J.ld_w = w->ld;
+  J.dim = x->cols;
   J.part = part;
   J.given = given;
   J.parts = P.parts;
@@ -260,8 +265,12 @@ fs_status forward(const fs_matrix* x, const fs_matrix* w, float eps, const void*
   J.entropy = entropy;
   J.lse = lse;
   J.stats = reinterpret_cast<float2*>(stats);
-  return launch("fs_linear_logprobs (join)", linear_join_kernel,
-                dim3(static_cast<unsigned>(ceil_div(x->rows, 8))), 256, 0, st, 1, J);
+  const char* what = "fs_linear_logprobs (join)";
+  if (x->rows <= sms)  // a CTA each
+    return launch(what, linear_join_kernel<8>, dim3(static_cast<unsigned>(x->rows)), 256, 0, st, 1,
+                  J);
+  return launch(what, linear_join_kernel<1>, dim3(static_cast<unsigned>(ceil_div(x->rows, 8))), 256,
+                0, st, 1, J);
 }
 
 fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void* ids,

@@ -59,12 +59,6 @@ __device__ __forceinline__ float warp_maxf(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ float warp_sumf(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // Score of one logit in fp32; m and inv are the row's maximum and 1 / sum (softmax).
 __device__ __forceinline__ float route_score(float z, int kind, float m, float inv) {
   return kind == kScoreSigmoid ? __fdividef(1.0f, 1.0f + ex2(-z * kLog2e)) : ex2((z - m) * kLog2e) * inv;

@@ -121,4 +121,11 @@ __device__ __forceinline__ void row_split(const T* row, int cols, int& head, int
   nvec = (cols - head) / Elem<T>::kVec;
 }
 
+// The same sum in every lane.
+__device__ __forceinline__ float warp_sumf(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 }  // namespace fs

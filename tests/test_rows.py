@@ -354,6 +354,27 @@ def test_linear_in_a_graph_and_on_two_streams():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("dim", [256, 4091])
+def test_linear_token_that_has_nearly_all_the_probability(rows, dim):
+    """The given token's score is formed apart from the others: it has to take its own place in
+    the sum, or a probability near 1 would come out above 1 or with the error of a score."""
+    w = rand(500, dim, seed=71, dtype=BF, scale=1.0)
+    ids = randint(rows, 500)
+    x = (25.0 / dim * w[ids].float()).to(BF)  # the token's score is about 25, the others' 25 / sqrt(dim)
+    pad = torch.zeros(rows, 8 * -(-dim // 8), dtype=BF, device="cuda")
+    pad[:, :dim] = x
+    out = fs.linear_logprobs(pad[:, :dim], w, ids)
+    z = x.double().cpu() @ w.double().cpu().t()
+    ref = torch.log_softmax(z, 1).gather(1, ids.cpu()[:, None])[:, 0]
+    # of the numbers near 1: the sum's rounding (2^-24), two exponentials and a logarithm (2 ulp,
+    # 2^-23 each); of the rest of the sum, e to the error of a score, which is below dim / 16 cuts
+    # of 2^-23 of sums below 40
+    tol = 2.0**-24 + 3 * 2.0**-23 + ref.abs() * (dim / 16 * 40 * 2.0**-23 * 1.5)
+    err = (out.logprobs.double().cpu() - ref).abs()
+    assert (err <= tol).all(), (err / tol).max()
+
+
 # ---- routing -----------------------------------------------------------------------------------
 
 def check_route(z, k, grads=True, seed=0, **kw):
