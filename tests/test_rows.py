@@ -94,6 +94,17 @@ def test_gradient_of_a_broadcast_row_is_the_sum():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("vocab,top", [(7, 7), (33, 32), (1000, 5), (1000, 20), (5003, 8)])
+def test_tokens_alternatives_of_many_rows(dtype, vocab, top):
+    """Enough rows for four warps each; rows of ties and of masked scores, and rows that start
+    inside a vector."""
+    z = rand(2600, vocab + 3, seed=23, dtype=dtype)
+    z[::5] = torch.randint(0, 4, z[::5].shape, generator=torch.Generator().manual_seed(2)).to(z)
+    z[1::5][torch.rand(z[1::5].shape, generator=torch.Generator().manual_seed(3)).cuda() < 0.98] = -math.inf
+    check_tokens(z[:, 3:], randint(2600, vocab), top=top, grads=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_tokens_alternatives_of_unkind_rows(dtype):
     """Rows that defeat a bar taken from their beginning: ascending, all equal, a few values only,
     the best at the ends, and long rows with more of them than a warp sets aside at once."""
