@@ -532,8 +532,8 @@ struct LinJoinParams {
 // A warp's share (of W warps) of x . w in fp32, the same in every lane: products of bf16 are exact,
 // the sums rounded to nearest. Rows are 16-byte aligned.
 template <int W>
-__device__ __forceinline__ float lin_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t dim,
-                                         int share, int lane) {
+__device__ __forceinline__ float lin_dot(const __nv_bfloat16* x, const __nv_bfloat16* w,
+                                         int64_t dim, int share, int lane) {
   float s[8] = {};
   const int64_t vecs = dim / 8;
   for (int64_t v0 = share * 4 * 32 + lane; v0 < vecs; v0 += W * 4 * 32) {  // (eight reads at once)
@@ -558,10 +558,11 @@ __device__ __forceinline__ float lin_dot(const __nv_bfloat16* x, const __nv_bflo
   return warp_sumf(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
 }
 
-// W warps per row (8 where rows are few): the parts of all units, in the same order every time. The given token's score is formed again
-// without the accumulators' cuts and takes its place in the sum, so that its log probability, the
-// difference of the two, carries the error of the sum alone (4 x 128000 x 4096: 1.3e-6 -> 5e-7
-// relative at worst). The gradient's statistics stay those of the scores that it will form.
+// W warps per row (8 where rows are few): the parts of all units, in the same order every time.
+// The given token's score is formed again without the accumulators' cuts and takes its place in
+// the sum, so that its log probability, the difference of the two, carries the error of the sum
+// alone (4 x 128000 x 4096: 1.3e-6 -> 4e-7 relative at worst, with the second accumulator). The
+// gradient's statistics stay those of the scores that it will form.
 template <int W>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P) {
   static_assert(W == 1 || W == 8, "a warp or a CTA");
