@@ -466,9 +466,10 @@ FS_API fs_status fs_linear_logprobs(const fs_matrix* x, const fs_matrix* w, floa
 /*
  * Gradients of those: grad_x (rows, dim) = G w and grad_w (cols, dim) = G^T x, contiguous bf16,
  * either may be NULL; G_ij = dL/dz_ij by the formula of fs_token_logprobs_grad, rounded to bf16
- * as an operand of the products, which are summed in float32. The workspace holds G, at most
- * 1 GiB of it at a time (more columns are done in chunks). An id >= cols makes grad_w NaN, and
- * the row's grad_x.
+ * as an operand of the products, which are summed in float32. What that rounding leaves of the
+ * given token's entry, and of that of a token with more than 0.51 of the probability, is added to
+ * the sums in float32. The workspace holds G, at most 1 GiB of it at a time (more columns are done
+ * in chunks). An id >= cols makes grad_w NaN, and the row's grad_x.
  */
 FS_API size_t fs_linear_logprobs_grad_workspace_bytes(const fs_matrix* x, const fs_matrix* w);
 FS_API fs_status fs_linear_logprobs_grad(const fs_matrix* x, const fs_matrix* w, float eps,

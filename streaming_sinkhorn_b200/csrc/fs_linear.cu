@@ -159,7 +159,8 @@ ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
 // The gradient: columns of a chunk of G, and the K splits of dx.
 struct BackwardPlan {
   int64_t chunk, chunks, ld_g, splits;
-  size_t off_acc, total;
+  int64_t n_keys;  // of the sort: a power of two, at least the entries (2 a row)
+  size_t off_flags, off_keys, off_g, off_acc, total;
 };
 
 BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
@@ -187,11 +188,46 @@ BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
       p.splits = s;
     }
   }
-  const size_t g = static_cast<size_t>(rows) * p.ld_g * 2;
-  p.off_acc = round_up(kHeader + g, 256);
+  p.n_keys = 32;
+  while (p.n_keys < 2 * rows) p.n_keys *= 2;
+  p.off_flags = kHeader + round_up(static_cast<size_t>(rows) * 2 * sizeof(LinRest), 256);
+  p.off_keys = p.off_flags + round_up(std::min(p.chunk, cols), 256);
+  p.off_g = p.off_keys + round_up(p.n_keys * sizeof(uint64_t), 256);
+  p.off_acc = p.off_g + round_up(static_cast<size_t>(rows) * p.ld_g * 2, 256);
   const bool partial = p.splits > 1 || p.chunks > 1;
   p.total = round_up(p.off_acc + (partial ? static_cast<size_t>(p.splits) * rows * dim * 4 : 0), 256);
   return p;
+}
+
+// The entries of a chunk's columns that dw adds in fp32, in order, and their sums (fs_linear.cuh).
+fs_status rests(const BackwardPlan& p, const LinRest* rest, int64_t rows, int64_t col0, int64_t n,
+                const fs_matrix* x, uint64_t* keys, uint8_t* has_rest, __nv_bfloat16* gw, int sms,
+                cudaStream_t st) {
+  const char* what = "fs_linear_logprobs_grad (order)";
+  const int64_t entries = 2 * rows;
+  fs_status s;
+  if (p.n_keys <= kSortSmem) {
+    s = launch(what, linear_order_kernel, dim3(1), kSortBlock, 0, st, 1, rest, entries, col0, n, keys,
+               static_cast<int>(p.n_keys));
+  } else {
+    s = launch(what, linear_keys_kernel, dim3(static_cast<unsigned>(ceil_div(p.n_keys, 256))), 256, 0,
+               st, 1, rest, entries, col0, n, keys, p.n_keys);
+    const dim3 blocks(static_cast<unsigned>(p.n_keys / kSortSmem));
+    const dim3 pairs(static_cast<unsigned>(p.n_keys / 2 / 256));
+    if (s == FS_OK)
+      s = launch(what, bitonic_smem_kernel, blocks, kSortBlock, 0, st, 1, keys, int64_t(0));
+    for (int64_t k = 2 * kSortSmem; s == FS_OK && k <= p.n_keys; k <<= 1) {
+      for (int64_t j = k / 2; s == FS_OK && j >= kSortSmem; j >>= 1)
+        s = launch(what, bitonic_global_kernel, pairs, 256, 0, st, 1, keys, p.n_keys, k, j);
+      if (s == FS_OK) s = launch(what, bitonic_smem_kernel, blocks, kSortBlock, 0, st, 1, keys, k);
+    }
+  }
+  if (s != FS_OK) return s;
+  const int64_t ctas = std::min<int64_t>(ceil_div(entries, 8), int64_t(8) * sms);
+  return launch("fs_linear_logprobs_grad (rests)", linear_rests_kernel,
+                dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(ceil_div(x->cols, 256))), 256,
+                0, st, 1, static_cast<const uint64_t*>(keys), p.n_keys, rest,
+                static_cast<const __nv_bfloat16*>(x->data), x->ld, x->cols, gw, has_rest);
 }
 
 bool shape_ok(const fs_matrix* x, const fs_matrix* w) {
@@ -297,12 +333,16 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
   if (!ws || !aligned(ws, 256) || ws_bytes < p.total) return FS_ERR_WORKSPACE;
   unsigned char* base = static_cast<unsigned char*>(ws);
   unsigned* err = reinterpret_cast<unsigned*>(base);
-  __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(base + kHeader);
+  LinRest* rest = reinterpret_cast<LinRest*>(base + kHeader);
+  uint8_t* has_rest = base + p.off_flags;
+  uint64_t* keys = reinterpret_cast<uint64_t*>(base + p.off_keys);
+  __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(base + p.off_g);
   float* acc = reinterpret_cast<float*>(base + p.off_acc);
   const bool partial = p.splits > 1 || p.chunks > 1;
   __nv_bfloat16* gx = static_cast<__nv_bfloat16*>(grad_x);
   __nv_bfloat16* gw = static_cast<__nv_bfloat16*>(grad_w);
-  s = cuda_status(cudaMemsetAsync(base, 0, kHeader, st), "cudaMemsetAsync");
+  // the error word, the rows' entries (none yet) and the tokens' flags
+  s = cuda_status(cudaMemsetAsync(base, 0, p.off_keys, st), "cudaMemsetAsync");
   if (s != FS_OK) return s;
   const __nv_bfloat16* wd = static_cast<const __nv_bfloat16*>(w->data);
   const int cg = pair_of(rows);
@@ -337,6 +377,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     P.g_lse = g_lse;
     P.g_out = G;
     P.ld_g = p.ld_g;
+    P.rest = rest;
     const char* what = "fs_linear_logprobs_grad (scores)";
     s = cg == 1 ? launch_linear<256, 1, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st)
                 : launch_linear<256, 2, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st);
@@ -359,12 +400,21 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.acc = acc;
       Q.add = c > 0;
       Q.ld_out = dim;
+      Q.rest = rest;
+      Q.w = wd;
+      Q.ld_w = w->ld;
       what = "fs_linear_logprobs_grad (dx)";
       s = cg == 1 ? launch_linear<256, 1, false, true, kLinStore>(what, ma, mt, mb, Q, sms, st)
                   : launch_linear<256, 2, false, true, kLinStore>(what, ma, mt, mb, Q, sms, st);
       if (s != FS_OK) return s;
     }
     if (gw) {  // dw = G^T x: K runs down both
+      if (c > 0) {
+        s = cuda_status(cudaMemsetAsync(has_rest, 0, p.off_keys - p.off_flags, st), "cudaMemsetAsync");
+        if (s != FS_OK) return s;
+      }
+      s = rests(p, rest, rows, col0, n, x, keys, has_rest, gw + col0 * dim, sms, st);
+      if (s != FS_OK) return s;
       LinParams Q{};
       if ((s = make_map(&ma, G, rows, n, p.ld_g, 64)) != FS_OK) return s;
       if ((s = make_map(&mb, x->data, rows, dim, x->ld, 64)) != FS_OK) return s;
@@ -381,6 +431,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.err = err;
       Q.out = gw + col0 * dim;
       Q.ld_out = dim;
+      Q.has_rest = has_rest;
       what = "fs_linear_logprobs_grad (dw)";
       s = cw == 1 ? launch_linear<256, 1, true, true, kLinStore>(what, ma, ma, mb, Q, sms, st)
                   : launch_linear<256, 2, true, true, kLinStore>(what, ma, ma, mb, Q, sms, st);
@@ -391,7 +442,8 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     const int64_t count = rows * dim;
     s = launch("fs_linear_logprobs_grad (sum)", linear_reduce_kernel,
                dim3(static_cast<unsigned>(ceil_div(count, 1024))), 256, 0, st, 1,
-               static_cast<const float*>(acc), static_cast<int>(p.splits), count, gx);
+               static_cast<const float*>(acc), static_cast<int>(p.splits), count, dim,
+               static_cast<const LinRest*>(rest), wd, w->ld, gx);
     if (s != FS_OK) return s;
   }
   return launch("fs_linear_logprobs_grad (check)", linear_poison_kernel,

@@ -10,6 +10,12 @@
 // over a batch's size), and two products finish it: dx = G w and dw = G^T x. G lives in the
 // workspace, in chunks of columns when all of it would not fit the cap.
 //
+// Two entries of a row can make up most of it: the given token's and that of a token with more
+// than half of the probability. Their rounding alone would be as large as that of the result (4096
+// x 65536 x 2048: 2.3e-3 of the gradients' norm against 1.65e-3 for exact G). So what it left is
+// kept in fp32 and added to the sums before they are rounded: r w[token] to dx, r x to dw[token],
+// the rows of one token in their order.
+//
 // One kernel does all four: C = A B^T over 64-wide K steps, warp 0 streams both operands
 // through a ring with TMA (128-byte swizzle), warp 1 issues the MMAs into one of two TMEM
 // accumulators, eight warps run the epilogue of the other (lane quarter warp % 4, half of the
@@ -35,6 +41,7 @@
 
 #include <cuda.h>
 
+#include "fs_bitonic.cuh"
 #include "fs_tcgen05.cuh"
 #include "fs_tokens.cuh"
 
@@ -69,6 +76,15 @@ struct LinShape {
   static_assert(ACCS == 1 || ACCS == KS, "an accumulator for each K step of a stage");
 };
 
+// One of the two entries of a row of G that are not left rounded.
+struct LinRest {
+  int32_t token;  // the entry's column + 1; 0: none
+  float rest;     // G - bf16(G)
+};
+// log2 of the probability above which a token's entry is kept (of one token at most, with room for
+// the rounding of p).
+constexpr float kLinLikely = -0.9714f;  // 0.51
+
 struct LinParams {
   int64_t m, n;        // rows of C, columns of C that exist
   int32_t k_steps;     // of the whole product
@@ -97,12 +113,41 @@ struct LinParams {
   const float* g_lse;
   __nv_bfloat16* g_out;
   int64_t ld_g;
+  LinRest* rest;  // (m, 2): the given token's, the likely token's; dx reads it
   // kLinStore
   __nv_bfloat16* out;  // bf16 output, or NULL: fp32 partial sums
   float* acc;          // (k_splits, m, n)
   int32_t add;         // add to acc (a later chunk)
   int64_t ld_out;
+  const __nv_bfloat16* w;  // dx straight to bf16: the embedding that the rests go with, or NULL
+  int64_t ld_w;
+  const uint8_t* has_rest;  // dw: whether the output row holds a sum to be added, or NULL
 };
+
+// Adds to 32 sums of a row of dx, from column `col` of `n`, its two rests times their tokens' rows
+// of w (16-byte aligned rows, col a multiple of 32).
+__device__ __forceinline__ void lin_add_rests(float* v, const LinRest* rest, const __nv_bfloat16* w,
+                                              int64_t ld_w, int64_t col, int64_t n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const LinRest e = rest[h];
+    if (e.token == 0 || e.rest == 0.0f) continue;
+    const __nv_bfloat16* src = w + static_cast<int64_t>(e.token - 1) * ld_w + col;
+    if (col + 32 <= n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float f[8];
+        Elem<__nv_bfloat16>::unpack(reinterpret_cast<const uint4*>(src)[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * j + i] = fmaf(e.rest, f[i], v[8 * j + i]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j < n) v[j] = fmaf(e.rest, __bfloat162float(src[j]), v[j]);
+    }
+  }
+}
 
 // Shared-memory matrix descriptor, 128-byte swizzle, sm_100 version field. K-major: lbo unused,
 // sbo = 1024 (8 rows of 128 bytes). MN-major: a box is 64 K rows of 64 elements; lbo = its size
@@ -429,12 +474,33 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           } else if constexpr (EPI == kLinScoreGrad) {
             const int64_t at = id - P.col0 - col;
             if (live && col < P.n) {
+              const int64_t in = P.n - col;  // columns from here on
+              int likely = -1;
+              float mx = fmaxf(v[0], v[1]);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : token_dscore(tr, v[j], k2, H);
-              if (at >= 0 && at < 32) {
+              for (int j = 2; j < 32; j += 2) mx = max3(mx, v[j], v[j + 1]);
+              if (!zero && (mx - tr.m) * k2 - tr.log2_l > kLinLikely) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (at == j) v[j] += hot;
+                  if (j < in && (v[j] - tr.m) * k2 - tr.log2_l > kLinLikely) likely = j;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : token_dscore(tr, v[j], k2, H);
+              const bool here = at >= 0 && at < 32 && at < in;
+              if (here || likely >= 0) {
+                float g = 0.0f, l = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  if (at == j) g = v[j] += hot;
+                  if (likely == j) l = v[j];
+                }
+                const int32_t first = static_cast<int32_t>(P.col0 + col) + 1;
+                if (here)
+                  P.rest[2 * row] = {first + static_cast<int32_t>(at),
+                                     g - __bfloat162float(__float2bfloat16_rn(g))};
+                if (likely >= 0 && likely != at)
+                  P.rest[2 * row + 1] = {first + likely,
+                                         l - __bfloat162float(__float2bfloat16_rn(l))};
               }
               // (columns past the last one fall into the row's padding)
               uint4* o = reinterpret_cast<uint4*>(P.g_out + row * P.ld_g + col);
@@ -449,6 +515,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               }
               if (P.out) {
                 __nv_bfloat16* o = P.out + row * P.ld_out + col;
+                if (P.w) lin_add_rests(v, P.rest + 2 * row, P.w, P.ld_w, col, P.n);
+                if (P.has_rest && P.has_rest[row]) {
+                  if (col + 32 <= P.n && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                      float f[8];
+                      Elem<__nv_bfloat16>::unpack(reinterpret_cast<const uint4*>(o)[j], f);
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+                    }
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                      if (col + j < P.n) v[j] += __bfloat162float(o[j]);
+                  }
+                }
                 if (col + 32 <= P.n && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
@@ -622,9 +704,171 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P)
   if (P.stats) P.stats[row] = bad ? make_float2(nan, nan) : make_float2(s.m, log_l);
 }
 
-// out = bf16 of the sum of the splits' fp32 partial products, in their order.
+// ---- the entries of G that are not left rounded --------------------------------------------------
+//
+// dx takes its two entries a row where its sums end (lin_add_rests). For dw the entries of a chunk
+// of columns are put in order of their tokens, and of rows where those are equal, so that each
+// token's are added up in the same order on every call: a sum of atomics would not repeat.
+
+// The sort key of entry e (of 2 a row), or the largest one if it has no token in the chunk.
+__device__ __forceinline__ uint64_t lin_rest_key(const LinRest* rest, int64_t e, int64_t entries,
+                                                 int64_t col0, int64_t n) {
+  if (e >= entries) return ~0ull;
+  const LinRest r = rest[e];
+  const int64_t col = static_cast<int64_t>(r.token) - 1 - col0;
+  if (r.token == 0 || r.rest == 0.0f || col < 0 || col >= n) return ~0ull;
+  return static_cast<uint64_t>(col) << 32 | static_cast<uint64_t>(e);
+}
+
+// All of them in order by one CTA: n_keys (a power of two, at most kSortSmem) >= entries.
+__global__ void __launch_bounds__(kSortBlock)
+    linear_order_kernel(const LinRest* rest, int64_t entries, int64_t col0, int64_t n,
+                        uint64_t* keys, int n_keys) {
+  __shared__ uint64_t s[kSortSmem];
+  const int t = threadIdx.x;
+  for (int e = t; e < n_keys; e += kSortBlock) s[e] = lin_rest_key(rest, e, entries, col0, n);
+  __syncthreads();
+  for (int k = 2; k <= n_keys; k <<= 1)
+    for (int j = k / 2; j > 0; j >>= 1) {
+      const int i = 2 * t - (t & (j - 1));
+      if (i + j < n_keys) cmp_swap(s[i], s[i + j], (i & k) == 0);
+      __syncthreads();
+    }
+  for (int e = t; e < n_keys; e += kSortBlock) keys[e] = s[e];
+}
+
+// More of them: the keys, which the bitonic kernels then sort.
 __global__ void __launch_bounds__(256)
-    linear_reduce_kernel(const float* acc, int splits, int64_t count, __nv_bfloat16* out) {
+    linear_keys_kernel(const LinRest* rest, int64_t entries, int64_t col0, int64_t n,
+                       uint64_t* keys, int64_t n_keys) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (e < n_keys) keys[e] = lin_rest_key(rest, e, entries, col0, n);
+}
+
+// Adds r x, from column d, of the entries whose keys are at [b, b + 32) and of token `col` to this
+// lane's 8 sums; their number. Up to 8 rows of x are on their way at once. Called by a whole warp.
+__device__ __forceinline__ int lin_rests_of(const uint64_t* keys, int64_t n_keys, int64_t b,
+                                            uint32_t col, const LinRest* rest,
+                                            const __nv_bfloat16* x, int64_t ld_x, int64_t d,
+                                            int64_t dim, float* sum, int lane) {
+  const uint64_t k = b + lane < n_keys ? keys[b + lane] : ~0ull;
+  const bool mine = static_cast<uint32_t>(k >> 32) == col && k != ~0ull;
+  const uint32_t e = mine ? static_cast<uint32_t>(k) : 0u;
+  const float r = mine ? rest[e].rest : 0.0f;
+  const int count = __popc(__ballot_sync(0xffffffffu, mine));  // (sorted: the first ones)
+#pragma unroll 1
+  for (int t0 = 0; t0 < count; t0 += 8) {
+    uint4 q[8];
+    float f[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int at = min(t0 + t, count - 1);  // (the last one again, times 0)
+      const float ft = __shfl_sync(0xffffffffu, r, at);
+      const uint32_t row = __shfl_sync(0xffffffffu, e, at) >> 1;
+      f[t] = t0 + t < count ? ft : 0.0f;
+      const __nv_bfloat16* src = x + static_cast<int64_t>(row) * ld_x + d;
+      if (d + 8 <= dim) {
+        q[t] = *reinterpret_cast<const uint4*>(src);
+      } else {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d + i < dim)
+            w[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(src[i])) << (16 * (i & 1));
+        q[t] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      float v[8];
+      Elem<__nv_bfloat16>::unpack(q[t], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(f[t], v[i], sum[i]);
+    }
+  }
+  return count;
+}
+
+__device__ __forceinline__ void lin_rests_write(const float* sum, __nv_bfloat16* o, int64_t d,
+                                                int64_t dim) {
+  if (d + 8 <= dim && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+    *reinterpret_cast<uint4*>(o) = Elem<__nv_bfloat16>::pack(sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (d + i < dim) o[i] = __float2bfloat16_rn(sum[i]);
+  }
+}
+
+// The sums r x of each token of the chunk that has entries, rounded to bf16 (2^-8 of what is at
+// most 2^-8 of the gradient) into its row of dw, where the product's epilogue adds them: no room of
+// their own, which would be another matrix of the gradient's size. A warp takes a token's first key
+// and 256 columns (grid y); a token with more than kLinMany entries is left to all warps of the
+// CTA, 32 entries each in turn (4096 x 65536 x 2048: 28 us after 38 for the order, of 3.8 ms; 86
+// with one token for all rows, 2041 by a warp).
+constexpr int kLinMany = 64;
+constexpr int kLinQueue = 64;
+
+__global__ void __launch_bounds__(256)
+    linear_rests_kernel(const uint64_t* keys, int64_t n_keys, const LinRest* rest,
+                        const __nv_bfloat16* x, int64_t ld_x, int64_t dim, __nv_bfloat16* out,
+                        uint8_t* has_rest) {
+  __shared__ int64_t queue[kLinQueue];
+  __shared__ int queued;
+  __shared__ float part[8][32][9];  // (rows of 9: no two lanes of a quarter on a bank)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t d = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+  if (threadIdx.x == 0) queued = 0;
+  __syncthreads();
+  for (int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + warp; p < n_keys; p += warps) {
+    const uint64_t key = keys[p];
+    if (key == ~0ull) break;  // (no entries from here on)
+    const uint32_t col = static_cast<uint32_t>(key >> 32);
+    if (p > 0 && static_cast<uint32_t>(keys[p - 1] >> 32) == col) continue;
+    if (p + kLinMany < n_keys && keys[p + kLinMany] != ~0ull &&
+        static_cast<uint32_t>(keys[p + kLinMany] >> 32) == col) {
+      int at = 0;
+      if (lane == 0) {
+        at = atomicAdd(&queued, 1);
+        if (at < kLinQueue) queue[at] = p;
+      }
+      if (__shfl_sync(0xffffffffu, at, 0) < kLinQueue) continue;
+    }
+    float sum[8] = {};
+    for (int64_t b = p; b < n_keys; b += 32)
+      if (lin_rests_of(keys, n_keys, b, col, rest, x, ld_x, d, dim, sum, lane) < 32) break;
+    lin_rests_write(sum, out + static_cast<int64_t>(col) * dim + d, d, dim);
+    if (blockIdx.y == 0 && lane == 0) has_rest[col] = 1;
+  }
+  __syncthreads();
+  const int n = min(queued, kLinQueue);
+  for (int q = 0; q < n; ++q) {
+    const int64_t p = queue[q];
+    const uint32_t col = static_cast<uint32_t>(keys[p] >> 32);
+    float sum[8] = {};
+    for (int64_t b = p + warp * 32; b < n_keys; b += 256)
+      if (lin_rests_of(keys, n_keys, b, col, rest, x, ld_x, d, dim, sum, lane) < 32) break;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[warp][lane][i] = sum[i];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        for (int w = 1; w < 8; ++w) sum[i] += part[w][lane][i];
+      lin_rests_write(sum, out + static_cast<int64_t>(col) * dim + d, d, dim);
+      if (blockIdx.y == 0 && lane == 0) has_rest[col] = 1;
+    }
+    __syncthreads();
+  }
+}
+
+// dx = bf16 of the sum of the splits' fp32 partial products, in their order, and of the row's two
+// entries that were not left rounded.
+__global__ void __launch_bounds__(256)
+    linear_reduce_kernel(const float* acc, int splits, int64_t count, int64_t dim,
+                         const LinRest* rest, const __nv_bfloat16* w, int64_t ld_w,
+                         __nv_bfloat16* out) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= count) return;
   float v[4];
@@ -643,7 +887,20 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < left; ++j) v[j] += p[j];
     }
   }
-  for (int j = 0; j < left; ++j) out[i + j] = __float2bfloat16_rn(v[j]);
+  int64_t row = i / dim, col = i - row * dim;
+  for (int j = 0; j < left; ++j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const LinRest e = rest[2 * row + h];
+      if (e.token != 0 && e.rest != 0.0f)
+        v[j] = fmaf(e.rest, __bfloat162float(w[static_cast<int64_t>(e.token - 1) * ld_w + col]), v[j]);
+    }
+    out[i + j] = __float2bfloat16_rn(v[j]);
+    if (++col == dim) {
+      col = 0;
+      ++row;
+    }
+  }
 }
 
 // After a wait that expired: NaN in place of the gradients.

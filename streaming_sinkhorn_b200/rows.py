@@ -331,7 +331,8 @@ def linear_logprobs(x, w, ids, *, eps: float = 1.0) -> LinearLogprobs:
     addresses are not multiples of 16 bytes are copied first); ids and eps as in
     token_logprobs. Scores are exact products summed in float32. Differentiable for x and w
     through logprobs, entropy and lse; the scores' gradient is rounded to bfloat16 as an
-    operand of the two products.
+    operand of the two products, except for the given token and one with more than half of
+    the probability.
     """
     x, w = _operand(x, "x"), _operand(w, "w")
     torch = _torch()
