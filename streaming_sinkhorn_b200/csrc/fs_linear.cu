@@ -114,6 +114,10 @@ fs_status launch_linear(const char* what, const CUtensorMap& a, const CUtensorMa
 // CTAs that share a tile of a product with this many rows: pairs once a pair has rows for both.
 int pair_of(int64_t rows) { return rows > kLinM ? 2 : 1; }
 
+// Width of a tile of scores. One row block reads w once and is bound by that read: narrow tiles
+// spread it evenly over the SMs. More row blocks are bound by the products: wide tiles.
+int tile_of(int cg) { return cg == 1 ? 128 : 256; }
+
 // The forward pass: tile width, column tiles of a unit, and how many units share a row block.
 struct ForwardPlan {
   int bn;
@@ -127,9 +131,7 @@ ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
   ForwardPlan p{};
   p.cg = pair_of(rows);
   p.m_blocks = ceil_div(rows, kLinM * p.cg);
-  // One row block reads w once and is bound by that read: narrow tiles spread it evenly over
-  // the SMs. More row blocks are bound by the products: wide tiles.
-  p.bn = p.cg == 1 ? 128 : 256;
+  p.bn = tile_of(p.cg);
   p.n_blocks = ceil_div(cols, p.bn);
   // The split of the columns whose last wave is fullest, of those that fill 1 .. 16 waves; ties go
   // to fewer parts.
@@ -346,6 +348,10 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
   if (s != FS_OK) return s;
   const __nv_bfloat16* wd = static_cast<const __nv_bfloat16*>(w->data);
   const int cg = pair_of(rows);
+  // the scores' tiles are the forward pass's, so that each score is cut in the same places and p
+  // goes with the row's sums (states of 4096, a token with all but 5e-5 of the probability: 1 - p
+  // was off by more than itself where a lone row block's scores were formed in wider tiles)
+  const int bn = tile_of(cg);
   for (int64_t c = 0; c < p.chunks; ++c) {
     const int64_t col0 = c * p.chunk;
     const int64_t n = std::min(p.chunk, cols - col0);
@@ -354,13 +360,13 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     LinParams P{};
     s = make_rows_maps(&ma, &mt, &P.tail_rows, x->data, rows, dim, x->ld);
     if (s != FS_OK) return s;
-    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, 256 / cg)) != FS_OK) return s;
+    if ((s = make_map(&mb, wd + col0 * w->ld, n, dim, w->ld, bn / cg)) != FS_OK) return s;
     P.m = rows;
     P.n = n;
     P.k_steps = static_cast<int32_t>(ceil_div(dim, kLinK));
     P.m_blocks = static_cast<int32_t>(ceil_div(rows, kLinM * cg));
     P.last_block = static_cast<int32_t>(ceil_div(rows, kLinM) - 1);
-    P.n_blocks = static_cast<int32_t>(ceil_div(n, 256));
+    P.n_blocks = static_cast<int32_t>(ceil_div(n, bn));
     P.n_per_unit = 1;
     P.k_splits = 1;
     P.units = static_cast<int64_t>(P.m_blocks) * P.n_blocks;
@@ -379,7 +385,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     P.ld_g = p.ld_g;
     P.rest = rest;
     const char* what = "fs_linear_logprobs_grad (scores)";
-    s = cg == 1 ? launch_linear<256, 1, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st)
+    s = cg == 1 ? launch_linear<128, 1, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st)
                 : launch_linear<256, 2, false, false, kLinScoreGrad>(what, ma, mt, mb, P, sms, st);
     if (s != FS_OK) return s;
     if (gx) {  // dx = G w: K runs along G's rows and down w's
