@@ -469,7 +469,8 @@ FS_API fs_status fs_linear_logprobs(const fs_matrix* x, const fs_matrix* w, floa
  * as an operand of the products, which are summed in float32. What that rounding leaves of the
  * given token's entry, and of that of a token with more than 0.51 of the probability, is added to
  * the sums in float32. The workspace holds G, at most 1 GiB of it at a time (more columns are done
- * in chunks). An id >= cols makes grad_w NaN, and the row's grad_x.
+ * in chunks), and a copy of x. An id >= cols makes grad_w NaN, and the row's grad_x; a row with a
+ * negative id has grad_x 0 and no part in grad_w, whatever x holds there.
  */
 FS_API size_t fs_linear_logprobs_grad_workspace_bytes(const fs_matrix* x, const fs_matrix* w);
 FS_API fs_status fs_linear_logprobs_grad(const fs_matrix* x, const fs_matrix* w, float eps,

@@ -162,7 +162,8 @@ ForwardPlan forward_plan(int64_t rows, int64_t cols, int sms) {
 struct BackwardPlan {
   int64_t chunk, chunks, ld_g, splits;
   int64_t n_keys;  // of the sort: a power of two, at least the entries (2 a row)
-  size_t off_flags, off_keys, off_g, off_acc, total;
+  int64_t ld_x;    // of the states copied for dw
+  size_t off_flags, off_x, off_keys, off_g, off_acc, total;
 };
 
 BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
@@ -193,7 +194,9 @@ BackwardPlan backward_plan(int64_t rows, int64_t cols, int64_t dim, int sms) {
   p.n_keys = 32;
   while (p.n_keys < 2 * rows) p.n_keys *= 2;
   p.off_flags = kHeader + round_up(static_cast<size_t>(rows) * 2 * sizeof(LinRest), 256);
-  p.off_keys = p.off_flags + round_up(std::min(p.chunk, cols), 256);
+  p.ld_x = round_up(dim, 8);
+  p.off_x = p.off_flags + round_up(std::min(p.chunk, cols), 256);
+  p.off_keys = p.off_x + round_up(static_cast<size_t>(rows) * p.ld_x * 2, 256);
   p.off_g = p.off_keys + round_up(p.n_keys * sizeof(uint64_t), 256);
   p.off_acc = p.off_g + round_up(static_cast<size_t>(rows) * p.ld_g * 2, 256);
   const bool partial = p.splits > 1 || p.chunks > 1;
@@ -344,9 +347,20 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
   __nv_bfloat16* gx = static_cast<__nv_bfloat16*>(grad_x);
   __nv_bfloat16* gw = static_cast<__nv_bfloat16*>(grad_w);
   // the error word, the rows' entries (none yet) and the tokens' flags
-  s = cuda_status(cudaMemsetAsync(base, 0, p.off_keys, st), "cudaMemsetAsync");
+  s = cuda_status(cudaMemsetAsync(base, 0, p.off_x, st), "cudaMemsetAsync");
   if (s != FS_OK) return s;
   const __nv_bfloat16* wd = static_cast<const __nv_bfloat16*>(w->data);
+  // dw's operand: the states of the rows that are asked about. (A row that is not has G = 0, but 0
+  // times what a batch's padding may hold need not be 0.)
+  __nv_bfloat16* xm = reinterpret_cast<__nv_bfloat16*>(base + p.off_x);
+  if (gw) {
+    const int64_t vecs = rows * (p.ld_x / 8);
+    s = launch("fs_linear_logprobs_grad (states)", linear_asked_kernel,
+               dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(vecs, 256), int64_t(16) * sms))),
+               256, 0, st, 1, static_cast<const __nv_bfloat16*>(x->data), x->ld, rows, dim, ids,
+               ids_64, xm, p.ld_x);
+    if (s != FS_OK) return s;
+  }
   const int cg = pair_of(rows);
   // the scores' tiles are the forward pass's, so that each score is cut in the same places and p
   // goes with the row's sums (states of 4096, a token with all but 5e-5 of the probability: 1 - p
@@ -406,6 +420,8 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
       Q.acc = acc;
       Q.add = c > 0;
       Q.ld_out = dim;
+      Q.ids = ids;
+      Q.ids_wide = ids_64;
       Q.rest = rest;
       Q.w = wd;
       Q.ld_w = w->ld;
@@ -416,14 +432,14 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     }
     if (gw) {  // dw = G^T x: K runs down both
       if (c > 0) {
-        s = cuda_status(cudaMemsetAsync(has_rest, 0, p.off_keys - p.off_flags, st), "cudaMemsetAsync");
+        s = cuda_status(cudaMemsetAsync(has_rest, 0, p.off_x - p.off_flags, st), "cudaMemsetAsync");
         if (s != FS_OK) return s;
       }
       s = rests(p, rest, rows, col0, n, x, keys, has_rest, gw + col0 * dim, sms, st);
       if (s != FS_OK) return s;
       LinParams Q{};
       if ((s = make_map(&ma, G, rows, n, p.ld_g, 64)) != FS_OK) return s;
-      if ((s = make_map(&mb, x->data, rows, dim, x->ld, 64)) != FS_OK) return s;
+      if ((s = make_map(&mb, xm, rows, dim, p.ld_x, 64)) != FS_OK) return s;
       Q.m = n;
       Q.n = dim;
       Q.k_steps = static_cast<int32_t>(ceil_div(rows, kLinK));
@@ -449,7 +465,7 @@ fs_status backward(const fs_matrix* x, const fs_matrix* w, float eps, const void
     s = launch("fs_linear_logprobs_grad (sum)", linear_reduce_kernel,
                dim3(static_cast<unsigned>(ceil_div(count, 1024))), 256, 0, st, 1,
                static_cast<const float*>(acc), static_cast<int>(p.splits), count, dim,
-               static_cast<const LinRest*>(rest), wd, w->ld, gx);
+               ids, ids_64, static_cast<const LinRest*>(rest), wd, w->ld, gx);
     if (s != FS_OK) return s;
   }
   return launch("fs_linear_logprobs_grad (check)", linear_poison_kernel,

@@ -416,6 +416,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       float H = 0.0f, hot = 0.0f;
       bool zero = true;
       if (EPI != kLinStore && live) id = ld_id(P.ids, row, P.ids_wide != 0);
+      // (dx: 0 whatever w holds)
+      const bool unasked =
+          EPI == kLinStore && P.w && live && ld_id(P.ids, row, P.ids_wide != 0) < 0;
       if (EPI == kLinScoreGrad && live && id >= 0) {
         const float2 st = P.stats[row];
         float gl = P.g_logp ? P.g_logp[row] : 0.0f;
@@ -515,7 +518,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               }
               if (P.out) {
                 __nv_bfloat16* o = P.out + row * P.ld_out + col;
-                if (P.w) lin_add_rests(v, P.rest + 2 * row, P.w, P.ld_w, col, P.n);
+                if (P.w) {
+                  lin_add_rests(v, P.rest + 2 * row, P.w, P.ld_w, col, P.n);
+                  if (unasked) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                  }
+                }
                 if (P.has_rest && P.has_rest[row]) {
                   if (col + 32 <= P.n && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
 #pragma unroll
@@ -710,6 +719,32 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P)
 // of columns are put in order of their tokens, and of rows where those are equal, so that each
 // token's are added up in the same order on every call: a sum of atomics would not repeat.
 
+// The states with rows that nobody asks about, and the padding, as zeros: 16 bytes a thread and step.
+__global__ void __launch_bounds__(256)
+    linear_asked_kernel(const __nv_bfloat16* x, int64_t ld_x, int64_t rows, int64_t dim,
+                        const void* ids, int ids_wide, __nv_bfloat16* out, int64_t ld_out) {
+  const int64_t per = ld_out / 8, count = rows * per;
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < count;
+       v += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = v / per, d = (v - row * per) * 8;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (ld_id(ids, row, ids_wide != 0) >= 0) {
+      const __nv_bfloat16* src = x + row * ld_x + d;
+      if (d + 8 <= dim) {
+        q = *reinterpret_cast<const uint4*>(src);
+      } else {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d + i < dim)
+            w[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(src[i])) << (16 * (i & 1));
+        q = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + row * ld_out + d) = q;
+  }
+}
+
 // The sort key of entry e (of 2 a row), or the largest one if it has no token in the chunk.
 __device__ __forceinline__ uint64_t lin_rest_key(const LinRest* rest, int64_t e, int64_t entries,
                                                  int64_t col0, int64_t n) {
@@ -864,10 +899,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // dx = bf16 of the sum of the splits' fp32 partial products, in their order, and of the row's two
-// entries that were not left rounded.
+// entries that were not left rounded; 0 for a row that nobody asks about.
 __global__ void __launch_bounds__(256)
-    linear_reduce_kernel(const float* acc, int splits, int64_t count, int64_t dim,
-                         const LinRest* rest, const __nv_bfloat16* w, int64_t ld_w,
+    linear_reduce_kernel(const float* acc, int splits, int64_t count, int64_t dim, const void* ids,
+                         int ids_wide, const LinRest* rest, const __nv_bfloat16* w, int64_t ld_w,
                          __nv_bfloat16* out) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= count) return;
@@ -895,7 +930,7 @@ __global__ void __launch_bounds__(256)
       if (e.token != 0 && e.rest != 0.0f)
         v[j] = fmaf(e.rest, __bfloat162float(w[static_cast<int64_t>(e.token - 1) * ld_w + col]), v[j]);
     }
-    out[i + j] = __float2bfloat16_rn(v[j]);
+    out[i + j] = __float2bfloat16_rn(ld_id(ids, row, ids_wide != 0) < 0 ? 0.0f : v[j]);
     if (++col == dim) {
       col = 0;
       ++row;
