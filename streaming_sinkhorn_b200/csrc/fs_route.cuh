@@ -8,11 +8,12 @@
 //
 // Which experts are picked is decided at borders, and a border that two implementations
 // round differently sends a token elsewhere. So the choice is the one of c in 64 bits: the
-// fast path works in fp32 with a bound on its error, and a row in which two neighbours of
-// the order (the last pick and the first that is left included) lie within their bounds is
-// done over in 64 bits by the same warp. Experts of equal logit and bias are equal in any
-// precision and need no second look. About one row in 1000 is done over on normal logits of
-// 256 experts.
+// fast path works in fp32 with a bound on its error, and a row in which two neighbours among the
+// picks, or the last pick and any expert that is left, lie within their bounds is done over in 64
+// bits by the same warp. (Any: bounds differ, and an expert behind the first one left, with a
+// larger bound or behind a tie, may be the better one.) Experts of equal logit and bias are equal
+// in any precision and need no second look. About one row in 1000 is done over on normal logits
+// of 256 experts.
 //
 // One warp takes a row, each lane a few neighbouring experts. What bounds it is instructions: 815
 // a row at 256 experts, 8 of them picked out of 4 of 8 groups (32768 rows: 46 us, the read of the
@@ -76,6 +77,16 @@ __device__ __forceinline__ double route_score64(double z, int kind, double m, do
 __device__ __forceinline__ float route_err(float z, float s, float c, bool sig, float m) {
   constexpr float u = 1.5f * 0x1p-24f;
   const float e = sig ? s * ((1.0f - s) * (2.0f * fabsf(z) + 4.0f) + 5.0f) : s * (3.0f * (m - z) + 45.0f);
+  return e * u + fabsf(c) * u + 0x1p-124f;
+}
+// The same for every expert whose c is not above this one's. c + |c| u grows with c. Without a
+// bias s is not above this one's either, and the bounds grow with s: softmax's for all s <= inv,
+// sigmoid's s (2 |z| + 9) for z <= 0; none is above 6.5 for sigmoid, 48 inv for softmax.
+__device__ __forceinline__ float route_left_err(float z, float s, float c, bool sig, float m,
+                                                float inv, bool biased) {
+  constexpr float u = 1.5f * 0x1p-24f;
+  const float e = sig ? (biased || z > 0.0f ? 6.5f : s * (2.0f * fabsf(z) + 9.0f))
+                      : (biased ? 48.0f * inv : s * (3.0f * (m - z) + 45.0f));
   return e * u + fabsf(c) * u + 0x1p-124f;
 }
 // The same for the sum of a group's two best, whichever they are: s (1 - s) (2 |z| + 4) <= 1.5
@@ -403,8 +414,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kerne
     int mine = -1;
     float cr = -INFINITY;
     float zr = 0.0f, s = 0.0f, br = 0.0f, err = 0.0f;
-    if (!(NL > 1 && P.k <= kRouteFew &&
-          route_pick_few<NL>(c, v, P.k, lane, reinterpret_cast<float4*>(c64), mine, cr, zr))) {
+    // what c still holds of the order: everything, or what is behind the first expert left out
+    const bool few = NL > 1 && P.k <= kRouteFew &&
+                     route_pick_few<NL>(c, v, P.k, lane, reinterpret_cast<float4*>(c64), mine, cr, zr);
+    if (!few) {
       route_pick_each<NL>(c, P.k, lane, mine, cr);
       if (mine >= 0) zr = Elem<T>::to_f(z[mine]);
     }
@@ -418,9 +431,29 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kerne
     const float nc = __shfl_down_sync(0xffffffffu, cr, 1);
     const float ne = __shfl_down_sync(0xffffffffu, err, 1);
     if (lane < P.k && mine >= 0) {
-      again |= nc != -INFINITY && !(cr - nc > err + ne) && !(zr == nz && br == nb);
+      again |= lane < P.k - 1 && nc != -INFINITY && !(cr - nc > err + ne) && !(zr == nz && br == nb);
       // a score that fp32 flushes also loses its weight
       again |= s < 0x1p-100f;
+    }
+    // experts that are left, with c so near the last pick's that they may belong before it
+    const float near = __shfl_sync(
+        0xffffffffu,
+        mine >= 0 ? cr - err - route_left_err(zr, s, cr, SIG, m, inv, P.bias != nullptr) : INFINITY,
+        P.k - 1);
+    int found = !few && lane == P.k && mine >= 0 && cr >= near ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) found += c[i] >= near ? 1 : 0;
+    again |= near != near;
+    if (__reduce_add_sync(0xffffffffu, found) > (few ? P.k : 0)) {
+      // all but those that equal it in any precision
+      const float lz = __shfl_sync(0xffffffffu, zr, P.k - 1);
+      const float lb = __shfl_sync(0xffffffffu, br, P.k - 1);
+      const float lc = __shfl_sync(0xffffffffu, cr, P.k - 1);
+      again |= !few && lane == P.k && mine >= 0 && cr >= near && !(zr == lz && br == lb);
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (c[i] >= near && c[i] <= lc)
+          again |= !(v[i] == lz && (!P.bias || (j0 + i < E && P.bias[j0 + i] == lb)));
     }
     if (__any_sync(0xffffffffu, again)) {
       route_row64(P, z, row, c64, hist, lane);
