@@ -89,11 +89,13 @@ __device__ __forceinline__ float route_left_err(float z, float s, float c, bool 
                       : (biased ? 48.0f * inv : s * (3.0f * (m - z) + 45.0f));
   return e * u + fabsf(c) * u + 0x1p-124f;
 }
-// The same for the sum of a group's two best, whichever they are: s (1 - s) (2 |z| + 4) <= 1.5
-// for sigmoid; s <= inv, the largest score, and s d <= inv for softmax.
-__device__ __forceinline__ float route_group_err(float sum, bool sig, float inv) {
+// The same for the sum of a group's two best, a and b (or a alone, b = -inf), whichever they are:
+// s (1 - s) (2 |z| + 4) <= 1.5 for sigmoid; s <= inv, the largest score, and s d <= inv for softmax.
+// Each has been rounded at its own size, and the sum at its.
+__device__ __forceinline__ float route_group_err(float a, float b, float sum, bool sig, float inv) {
   constexpr float u = 1.5f * 0x1p-24f;
-  return (2.0f * (sig ? 6.5f : 48.0f * inv) + 3.0f * fabsf(sum) + 4.0f) * u;
+  const float terms = fabsf(a) + (b == -INFINITY ? 0.0f : fabsf(b));
+  return (2.0f * (sig ? 6.5f : 48.0f * inv) + terms + fabsf(sum) + 4.0f) * u;
 }
 
 __device__ __forceinline__ float redux_max(float v) {
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kerne
       }
       const float gs = g >= P.groups ? -INFINITY : (b == -INFINITY ? a : a + b);
       // kept: the groups down to the top_groups-th largest sum; where equal sums make it more,
-      // or the next sum is near, 64 bits decide
+      // or one that is kept and one that is not are within their bounds, 64 bits decide
       float left = gs, lo = -INFINITY;
       for (int r = 0; r < P.top_groups; ++r) {
         const float t = redux_max(left);
@@ -391,9 +393,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NL <= 8 ? 5 : 1) route_kerne
         if (left == t) left = -INFINITY;
       }
       const bool kept = gs >= lo && gs != -INFINITY;
-      const float hi = redux_max(left);
-      again = (hi != -INFINITY && !(lo - hi > route_group_err(lo, SIG, inv) +
-                                                 route_group_err(hi, SIG, inv))) ||
+      const bool open = gs != -INFINITY;
+      const float ge = open ? route_group_err(a, b, gs, SIG, inv) : 0.0f;
+      const float hi = redux_max(open && !kept ? gs + ge : -INFINITY);
+      const float least = -redux_max(kept ? ge - gs : -INFINITY);
+      again = (hi != -INFINITY && !(least > hi)) ||
               __popc(__ballot_sync(0xffffffffu, kept && lane % lanes == 0)) > P.top_groups;
       if (by_lanes) {
         if (!kept) {
