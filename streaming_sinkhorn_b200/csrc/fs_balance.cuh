@@ -440,9 +440,14 @@ __global__ void __launch_bounds__(NW * 32, 1) balance_kernel(const BalanceParams
   // log2 beta, gamma of the start
   if (warp == 0) {
     double tot = 0.0;
+    bool bad = false;
     if (P.load)
-      for (int j = lane; j < E; j += 32) tot += P.load[j];
-    tot = warp_sum(tot);
+      for (int j = lane; j < E; j += 32) {
+        tot += P.load[j];
+        bad |= !(P.load[j] >= 0.0f && P.load[j] < INFINITY);
+      }
+    // (a sum of 0 makes every share NaN; so does a bad entry, those of an expert of load 0 too)
+    tot = __any_sync(0xffffffffu, bad) ? __longlong_as_double(0x7FF8000000000000ll) : warp_sum(tot);
     for (int j = lane; j < S::kCols; j += 32) {
       float b = 0.0f;
       if (j >= E)
