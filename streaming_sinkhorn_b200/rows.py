@@ -4,7 +4,8 @@ experts' load.
 
 Only argument marshalling happens here: every number comes from the C ABI. Unlike the solves,
 these calls are asynchronous (they enqueue on the current stream of the data's device and
-return) and can be captured into a CUDA graph. Gradients are analytic and differentiable once.
+return) and can be captured into a CUDA graph. Gradients are analytic and differentiable once;
+forward-mode derivatives are refused.
 """
 from __future__ import annotations
 
@@ -77,6 +78,10 @@ def _rows_of(t, name):
     if t.dim() != 2 or t.shape[1] < 1:
         raise ValueError(f"{name} must be a 2-D tensor with at least one column")
     _dtype_code(t.dtype, name)
+    # (a result without a tangent would read as a derivative of 0)
+    if torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+        raise NotImplementedError(f"{name} carries a forward-mode tangent: only reverse-mode "
+                                  "derivatives are supported")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if (t.stride(1) != 1 and t.shape[1] > 1) or (t.stride(0) < t.shape[1] and t.shape[0] > 1):
