@@ -52,15 +52,16 @@ class PerDeviceOnce {
   std::atomic<uint64_t> done_{0};
 };
 
-// CTAs of a kernel that an SM holds at once, asked once per kernel and device.
+// CTAs of a kernel that an SM holds at once with this much shared memory; the last answer for each
+// device is kept with its question.
 class PerDeviceOccupancy {
  public:
   int get(const void* fn, int threads, size_t smem) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 64;
     if (dev < 64) {
-      const int n = known_[dev].load(std::memory_order_relaxed);
-      if (n > 0) return n;
+      const uint64_t known = known_[dev].load(std::memory_order_relaxed);
+      if (known != 0 && known >> 8 == smem) return static_cast<int>(known & 255);
     }
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) {
@@ -68,12 +69,15 @@ class PerDeviceOccupancy {
       n = 1;
     }
     if (n < 1) n = 1;
-    if (dev < 64) known_[dev].store(n, std::memory_order_relaxed);
+    // (an SM holds 32 CTAs at most)
+    if (dev < 64 && n < 256)
+      known_[dev].store(static_cast<uint64_t>(smem) << 8 | static_cast<uint64_t>(n),
+                        std::memory_order_relaxed);
     return n;
   }
 
  private:
-  std::atomic<int> known_[64] = {};
+  std::atomic<uint64_t> known_[64] = {};
 };
 
 // Launches `kernel` (a cluster of `cluster` CTAs along x when cluster > 1; kCooperative: all
