@@ -390,7 +390,7 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
     if e > _lib.FS_MAX_EXPERTS:
         raise ValueError(f"{e} experts: at most {_lib.FS_MAX_EXPERTS} are supported")
     if bias is not None:
-        bias = _vector(bias.detach(), "bias", e, logits.device, (_torch().float32,))
+        bias = _vector(bias, "bias", e, logits.device, (_torch().float32,)).detach()
     k, groups, top_groups = int(k), int(groups), int(top_groups)
     if groups < 1 or groups > 32 or e % groups or not 1 <= top_groups <= groups:
         raise ValueError(f"{top_groups} of {groups} groups of {e} experts: groups must be 1..32 "
@@ -425,9 +425,9 @@ def balance(logits, *, score: str = "softmax", eps: float, n_iters: int, load=No
     if n < 1:
         raise ValueError("logits must have at least one row")
     if load is not None:
-        load = _vector(load.detach(), "load", e, dev, (torch.float32,))
+        load = _vector(load, "load", e, dev, (torch.float32,)).detach()
     if g_init is not None:
-        g_init = _vector(g_init.detach(), "g_init", e, dev, (torch.float32,))
+        g_init = _vector(g_init, "g_init", e, dev, (torch.float32,)).detach()
     f = torch.empty(n, dtype=torch.float32, device=dev)
     g = torch.empty(e, dtype=torch.float32, device=dev)
     lib = _lib.load()
