@@ -70,7 +70,8 @@ struct LinShape {
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
   // Two tiles' accumulators fill the tensor memory. Where a tile leaves room, the K steps of a
   // stage go to one each and meet in the epilogue: an accumulator's sum is cut to fp32 after every
-  // 16 products, always towards 0, and half as many of smaller sums cost 0.7 of the error.
+  // 16 products, always towards 0, and half as many of smaller sums cost less than half (what is
+  // left of the mean loss, the scores' factor puts back).
   static constexpr int ACCS = 512 / (2 * BN);
   static constexpr uint32_t TMEM = 512;
   static_assert(ACCS == 1 || ACCS == KS, "an accumulator for each K step of a stage");
@@ -97,6 +98,7 @@ struct LinParams {
   int64_t units;
   unsigned* err;
   float inv_eps;
+  float uncut;  // factor of the scores: puts back what the accumulators' cuts take of them
   const void* ids;
   int32_t ids_wide;
   // kLinLse
@@ -455,6 +457,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += v1[j];
           }
+          if constexpr (EPI != kLinStore) {
+            const u64 k = pk(P.uncut, P.uncut);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) upk(mul2(pk(v[j], v[j + 1]), k), v[j], v[j + 1]);
+          }
           const int64_t col = c0 + c;
           if constexpr (EPI == kLinLse) {
             if (col + 32 > P.n) {
@@ -652,8 +659,9 @@ __device__ __forceinline__ float lin_dot(const __nv_bfloat16* x, const __nv_bflo
 // W warps per row (8 where rows are few): the parts of all units, in the same order every time.
 // The given token's score is formed again without the accumulators' cuts and takes its place in
 // the sum, so that its log probability, the difference of the two, carries the error of the sum
-// alone (4 x 128000 x 4096: 1.3e-6 -> 4e-7 relative at worst, with the second accumulator). The
-// gradient's statistics stay those of the scores that it will form.
+// alone (4 x 128000 x 4096: 1.3e-6 -> 4e-7 relative at worst, with the second accumulator; 4e-8 with
+// the scores' factor). The gradient's statistics stay those of the scores that it will form, in the
+// same tiles.
 template <int W>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinJoinParams P) {
   static_assert(W == 1 || W == 8, "a warp or a CTA");
