@@ -295,7 +295,8 @@ struct BalancePlan {
 
 constexpr size_t kBalSmemBudget = 224u * 1024u;  // of 227 KB; the static part is 300 bytes
 
-constexpr int64_t kBalClusterScores = 640 * 1000;  // (balance_plan says why)
+// (balance_plan says why)
+constexpr int64_t kBalClusterScores = 660 * 1000, kBalClusterRows = 680;
 
 BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   BalancePlan p{};
@@ -314,11 +315,12 @@ BalancePlan balance_plan(int64_t rows, int64_t experts, bool allow_cluster) {
   };
   // A cluster exchanges its sums in less time than the grid's 4 us an iteration, but has only 16
   // SMs: it is taken, with fewer CTAs for fewer rows, while the exponentials of one iteration on
-  // those take less than what it saves, and shared memory holds them (10 iterations, us, cluster
-  // and grid: 512 x 16 20 and 43, 2048 x 64 26 and 47, 1000 x 256 40 and 48, 8191 x 64 44 and 48,
-  // 40000 x 16 46 and 49, 2000 x 256 51 and 49, 12000 x 64 54 and 49).
+  // those take less than what it saves, and shared memory holds them. Wide rows reach that sooner
+  // (10 iterations, us, cluster and grid: 512 x 16 23 and 48, 2048 x 64 30 and 51, 1000 x 256 43 and
+  // 53, 1600 x 256 51 and 55, 2000 x 256 55 and 54, 4000 x 128 50 and 53, 5000 x 128 55 and 53,
+  // 8191 x 64 47 and 51, 9000 x 64 52 and 53, 12000 x 64 59 and 53, 40000 x 16 50 and 52).
   p.cluster = false;
-  if (allow_cluster && p.nl == 8 && rows * p.cols <= kBalClusterScores) {
+  if (allow_cluster && p.nl == 8 && (rows + kBalClusterRows) * p.cols <= kBalClusterScores) {
     for (int c = 1; c <= kBalMaxCluster && !p.cluster; c *= 2) {
       if (c < kBalMaxCluster && rows > 2 * step * c) continue;
       if ((rows + c - 1) / c * row + cluster_fixed > kBalSmemBudget) continue;
