@@ -530,7 +530,8 @@ FS_API fs_status fs_route_grad(const fs_matrix* z, const fs_route_options* opt,
  * is: with that bias (g alone for a uniform load) fs_route's first pick follows the load as far
  * as the plan is sharp (small eps); for k > 1 the further picks are evened out only roughly.
  * Logits of -inf are closed (e^.. = 0), a row of nothing else takes no part and gets f = 0, a
- * column closed to every row g = 0, a column of load 0 g = -inf. NaN in z, or a load with a
+ * column closed to every row g = 0, a column of load 0 g = -inf; a row open to such columns alone
+ * adds nothing to any sum (it still counts among the rows) and gets f = 0. NaN in z, or a load with a
  * negative or infinite entry, NaN or sum 0, makes the outputs NaN. All iterations run in one cooperative
  * launch; its waits are bounded (2 s), and if one expires f and g are NaN.
  * ws: fs_balance_workspace_bytes(z) bytes (0 for a shape that is not taken), 256-byte aligned.
