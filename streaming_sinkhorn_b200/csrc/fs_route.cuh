@@ -15,9 +15,9 @@
 // in any precision and need no second look. About one row in 1000 is done over on normal logits
 // of 256 experts.
 //
-// One warp takes a row, each lane a few neighbouring experts. What bounds it is instructions: 815
-// a row at 256 experts, 8 of them picked out of 4 of 8 groups (32768 rows: 46 us, the read of the
-// logits alone 5), 460 at 64 experts.
+// One warp takes a row, each lane a few neighbouring experts. What bounds it is instructions: 895
+// a row at 256 experts, 8 of them picked out of 4 of 8 groups (32768 rows: 50 us, the read of the
+// logits alone 5), 513 at 64 experts (80 and 53 of them compare what is left with the last pick).
 #pragma once
 
 #include <cfloat>
@@ -287,8 +287,8 @@ __device__ __forceinline__ bool route_pick_few(const float* c, const float* z, i
 }
 
 // Picks of at most this many go by way of candidates where a lane holds several experts: at 256
-// experts 8 picks take 38 us that way and 48 one by one, 12 take 41 and 57; beyond, too many
-// experts reach the bar (32768 rows; 1 or 2 picks take the same time either way).
+// experts 8 picks take 34 us that way and 42 one by one, 12 take 39 and 54; beyond, too many
+// experts reach the bar (32768 rows; 1 or 2 picks take nearly the same time either way).
 constexpr int kRouteFew = 12;
 
 // NL: experts per lane, lane l holding l * NL .. + NL - 1. Dynamic shared memory: route_room

@@ -332,12 +332,13 @@ def _operand(t, name):
 def linear_logprobs(x, w, ids, *, eps: float = 1.0) -> LinearLogprobs:
     """token_logprobs(x @ w.T, ids) without the scores ever stored (fs_linear_logprobs).
 
-    x: (T, D) states and w: (V, D) embedding, bfloat16, rows any stride apart (rows whose
-    addresses are not multiples of 16 bytes are copied first); ids and eps as in
-    token_logprobs. Scores are exact products summed in float32. Differentiable for x and w
-    through logprobs, entropy and lse; the scores' gradient is rounded to bfloat16 as an
-    operand of the two products, except for the given token and one with more than half of
-    the probability.
+    x: (T, D) states and w: (V, D) embedding, bfloat16, rows any stride apart; ids and eps as in
+    token_logprobs. A matrix whose rows' addresses are not all multiples of 16 bytes (D no
+    multiple of 8, for one) is copied whole on every call, and the copy kept until the backward
+    pass: pad such an embedding once. The states of rows with a negative id may hold anything.
+    Scores are exact products summed in float32. Differentiable for x and w through logprobs,
+    entropy and lse; the scores' gradient is rounded to bfloat16 as an operand of the two
+    products, except for the given token and one with more than half of the probability.
     """
     x, w = _operand(x, "x"), _operand(w, "w")
     torch = _torch()
