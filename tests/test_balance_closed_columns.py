@@ -64,3 +64,26 @@ def test_closed_and_sharp_columns_match_float64(rows, experts, score):
     assert g[3].item() == 0.0 and g[experts - 1].item() == 0.0
     f, g = check_balance(z, eps, 4, score, load=load, g_init=rand(experts, seed=3, scale=0.1))
     assert g[3].item() == 0.0 and g[4].item() == -math.inf
+
+
+@pytest.mark.parametrize("rows,experts", [(700, 24), (20011, 60)])
+def test_captured_with_other_closed_columns_at_each_replay(rows, experts):
+    z = rand(rows, experts, seed=1, scale=1.0)
+    fs.balance(z, score="sigmoid", eps=0.004, n_iters=4)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fs.balance(z, score="sigmoid", eps=0.004, n_iters=4)
+    for seed in (2, 3):
+        z.copy_(rand(rows, experts, seed=seed, scale=2.0))
+        z[:, seed * 5] = -math.inf
+        graph.replay()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(check_balance(z, 0.004, 4, "sigmoid"))
+        torch.cuda.synchronize()
+        for f, g in got:
+            assert torch.equal(f, out[0]) and torch.equal(g, out[1])

@@ -106,3 +106,42 @@ def test_sorted_tokens_and_repeated_calls_agree_bit_by_bit():
     for _ in range(4):
         got = torch.autograd.grad(fs.linear_logprobs(x, w, ids).logprobs, leaves, g)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("rows", [90, 1500])
+def test_captured_with_other_tokens_at_each_replay(rows):
+    w, ids = few_words(rows, 3000, 72, 9, seed=51)
+    x = rand(rows, 72, seed=52, scale=0.05).to(BF).requires_grad_(True)
+    w.requires_grad_(True)
+    g = rand(rows, seed=53, scale=1.0)
+
+    def step():
+        return torch.autograd.grad(fs.linear_logprobs(x, w, ids).logprobs, (x, w), g)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (54, 55):
+        ids.copy_(randint(rows, 3000 if seed == 54 else 2, seed=seed))
+        ids[::4] = -1
+        x.data.copy_(rand(rows, 72, seed=seed, scale=0.05))
+        x.data[::4] = math.nan
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        for a, b in zip(out, want):
+            assert torch.isfinite(b).all() and torch.equal(a, b)
+        torch.cuda.synchronize()
+
+
+def test_more_rows_than_one_cta_sorts():
+    rows, cols, dim = 70001, 2000, 40
+    w, ids = few_words(rows, cols, dim, 300, seed=61)
+    ids[1::3] = -1
+    x = rand(rows, dim, seed=62, scale=0.05).to(BF)
+    check_rounding(x, w, ids, rand(rows, seed=63, scale=1.0))
