@@ -127,7 +127,8 @@ int tile_of(int cg) { return cg == 1 ? 128 : 256; }
 // score in 8 products at the beginning, the middle or the end of K the log-sum-exp's 2.7e-6, 1.5e-6,
 // 3.5e-7 without and 1.3e-6, 1.2e-7, 1.1e-6 with it.
 float uncut(int64_t dim, int cg) {
-  const double cuts = static_cast<double>(ceil_div(dim, 16)) / (cg == 1 ? 2 : 1);  // of an accumulator
+  const double accumulators = cg == 1 ? 2.0 : 1.0;
+  const double cuts = static_cast<double>(ceil_div(dim, 16)) / accumulators;
   return static_cast<float>(1.0 + cuts * 0x1p-23 / 8);
 }
 
@@ -225,11 +226,11 @@ fs_status rests(const BackwardPlan& p, const LinRest* rest, int64_t rows, int64_
   const int64_t entries = 2 * rows;
   fs_status s;
   if (p.n_keys <= kSortSmem) {
-    s = launch(what, linear_order_kernel, dim3(1), kSortBlock, 0, st, 1, rest, entries, col0, n, keys,
-               static_cast<int>(p.n_keys));
+    s = launch(what, linear_order_kernel, dim3(1), kSortBlock, 0, st, 1, rest, entries, col0, n,
+               keys, static_cast<int>(p.n_keys));
   } else {
-    s = launch(what, linear_keys_kernel, dim3(static_cast<unsigned>(ceil_div(p.n_keys, 256))), 256, 0,
-               st, 1, rest, entries, col0, n, keys, p.n_keys);
+    const dim3 each(static_cast<unsigned>(ceil_div(p.n_keys, 256)));
+    s = launch(what, linear_keys_kernel, each, 256, 0, st, 1, rest, entries, col0, n, keys, p.n_keys);
     const dim3 blocks(static_cast<unsigned>(p.n_keys / kSortSmem));
     const dim3 pairs(static_cast<unsigned>(p.n_keys / 2 / 256));
     if (s == FS_OK)

@@ -26,8 +26,8 @@
 // With more than 128 rows a pair of CTAs works on 256 x 256 tiles: each brings its own 128 rows
 // of A and half of B's 256, the first issues the MMAs of both, so B crosses from L2 once for 256
 // rows: a single CTA's 128 x 256 tile wants 96 bytes a clock of L2 at the tensor cores' rate, a
-// pair's 64 each (4096 x 65536 x 2048 with gradients takes 3.8 ms, with one CTA a tile 6 % more). That
-// is still what bounds the products: 8.6 GB from L2 in 770 to 840 us (10 to 11 TB/s), tensor pipes
+// pair's 64 each (4096 x 65536 x 2048 with gradients takes 3.8 ms, with one CTA a tile 6 % more).
+// That is still what bounds the products: 8.6 GB from L2 in 770 to 840 us (10 to 11 TB/s), tensor pipes
 // 67 to 77 % active, 1.30 to 1.42 PFLOP/s. Up to 128 rows w is read once and bounds the pass: 4 x
 // 128000 x 4096 takes 164 us, 6.4 TB/s.
 //
